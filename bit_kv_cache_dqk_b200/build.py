@@ -11,7 +11,8 @@ LIB = os.path.join(HERE, "libdualqk.so")
 ROOT = os.path.dirname(HERE)
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v"]
+              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v",
+              "--split-compile=0"]   # one translation unit: its kernels are optimised in parallel
 
 
 def sources() -> list[str]:

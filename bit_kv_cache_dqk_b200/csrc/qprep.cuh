@@ -131,6 +131,60 @@ __device__ __forceinline__ int count_ge(const uint32_t (&mag)[NG], bool ch0, uin
     return (int)__reduce_add_sync(0xffffffffu, n);
 }
 
+// Kept channels of one head, by a warp: channel 0 and the nk - 1 channels c >= 1
+// with the largest |q'_c| (fp32 magnitudes as bit patterns), ties to the lower
+// index; lane owns channels lane + 32 g, kmask[g] has the bit of channel
+// 32 g + bit.  T = the (nk-1)-th largest magnitude, found bit by bit from the
+// top (the largest T with at least nk - 1 magnitudes >= T); then every channel
+// above T is kept, and of those equal to T the lowest-indexed ones that
+// complete the count.
+template <int NG>
+__device__ __forceinline__ void select_kept(const float *qp, int nk, int lane, uint32_t (&kmask)[NG]) {
+    const int m = nk - 1;
+    uint32_t mag[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const int c = lane + 32 * g;
+        mag[g] = c == 0 ? 0u : (__float_as_uint(qp[c]) & 0x7fffffffu);
+    }
+    const bool ch0 = lane == 0;   // channel 0 (g = 0) takes no part
+    uint32_t T = 0;
+    int cnt = 32 * NG - 1;   // channels >= T
+    // bit 30 alone, then two bits per step (three candidates counted at
+    // once); done as soon as exactly m channels are >= T (the prefix then
+    // separates the kept channels from the others)
+    {
+        const int n = count_ge<NG>(mag, ch0, 1u << 30);
+        if (n >= m) {
+            T = 1u << 30;
+            cnt = n;
+        }
+    }
+#pragma unroll 1
+    for (int bit = 28; bit >= 0 && cnt != m; bit -= 2) {
+        const int n3 = count_ge<NG>(mag, ch0, T | (3u << bit)), n2 = count_ge<NG>(mag, ch0, T | (2u << bit)),
+                  n1 = count_ge<NG>(mag, ch0, T | (1u << bit));
+        const uint32_t d = n3 >= m ? 3u : n2 >= m ? 2u : n1 >= m ? 1u : 0u;
+        T |= d << bit;
+        cnt = d == 3u ? n3 : d == 2u ? n2 : d == 1u ? n1 : cnt;
+    }
+    // with cnt > m, T is the m-th largest magnitude itself and ties at T
+    // go to the lower channel indices
+    const bool exact = cnt == m;
+    int need = exact ? 0 : m - (T == 0x7fffffffu ? 0 : count_ge<NG>(mag, ch0, T + 1u));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const bool eq = !exact && mag[g] == T && !(g == 0 && ch0) && m > 0;
+        const uint32_t eqm = __ballot_sync(0xffffffffu, eq);
+        const int rank = __popc(eqm & ((1u << lane) - 1u));   // equal channels of lower index in this group
+        const bool above = exact ? mag[g] >= T : mag[g] > T;
+        const bool keep = (above && !(g == 0 && ch0) && m > 0) || (eq && rank < need);
+        kmask[g] = __ballot_sync(0xffffffffu, keep);
+        need -= __popc(eqm);
+    }
+    kmask[0] |= 1u;   // channel 0 is always kept
+}
+
 // The rare paths of the piece arithmetic (subnormal operands), kept out of
 // line: the prologue runs once per launch, so its code is fetched cold and
 // every inlined instruction costs.
@@ -215,56 +269,8 @@ __device__ void qprep_kv(const float *__restrict__ t_q, const void *__restrict__
     if (warp < G) {
         const int h = warp, hl = h, nt = hl >> 2, hh = hl & 3;
         const int hg = j * G + h;   // query head index
-        // selection of the nk - 1 channels c >= 1 with the largest |q'_c|
-        // (fp32 magnitudes as bit patterns), ties to the lower index; lane owns
-        // channels lane + 32 g.  T = the (nk-1)-th largest magnitude, found bit
-        // by bit from the top (the largest T with at least nk - 1 magnitudes >=
-        // T); then every channel above T is kept, and of those equal to T the
-        // lowest-indexed ones that complete the count.
-        const int m = nk - 1;
-        uint32_t mag[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int c = lane + 32 * g;
-            mag[g] = c == 0 ? 0u : (__float_as_uint(qpv[h * D + c]) & 0x7fffffffu);
-        }
-        const bool ch0 = lane == 0;   // channel 0 (g = 0) takes no part
-        uint32_t T = 0;
-        int cnt = D - 1;   // channels >= T
-        // bit 30 alone, then two bits per step (three candidates counted at
-        // once); done as soon as exactly m channels are >= T (the prefix then
-        // separates the kept channels from the others)
-        {
-            const int n = count_ge<NG>(mag, ch0, 1u << 30);
-            if (n >= m) {
-                T = 1u << 30;
-                cnt = n;
-            }
-        }
-#pragma unroll 1
-        for (int bit = 28; bit >= 0 && cnt != m; bit -= 2) {
-            const int n3 = count_ge<NG>(mag, ch0, T | (3u << bit)), n2 = count_ge<NG>(mag, ch0, T | (2u << bit)),
-                      n1 = count_ge<NG>(mag, ch0, T | (1u << bit));
-            const uint32_t d = n3 >= m ? 3u : n2 >= m ? 2u : n1 >= m ? 1u : 0u;
-            T |= d << bit;
-            cnt = d == 3u ? n3 : d == 2u ? n2 : d == 1u ? n1 : cnt;
-        }
-        // with cnt > m, T is the m-th largest magnitude itself and ties at T
-        // go to the lower channel indices
-        const bool exact = cnt == m;
-        int need = exact ? 0 : m - (T == 0x7fffffffu ? 0 : count_ge<NG>(mag, ch0, T + 1u));
         uint32_t kmask[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const bool eq = !exact && mag[g] == T && !(g == 0 && ch0) && m > 0;
-            const uint32_t eqm = __ballot_sync(0xffffffffu, eq);
-            const int rank = __popc(eqm & ((1u << lane) - 1u));   // equal channels of lower index in this group
-            const bool above = exact ? mag[g] >= T : mag[g] > T;
-            const bool keep = (above && !(g == 0 && ch0) && m > 0) || (eq && rank < need);
-            kmask[g] = __ballot_sync(0xffffffffu, keep);
-            need -= __popc(eqm);
-        }
-        kmask[0] |= 1u;   // channel 0 is always kept
+        select_kept<NG>(qpv + h * D, nk, lane, kmask);
 
         // lane owns channels lane + 32 g: scaled q' on kept channels >= 1, group
         // sums and maxima, sigma_h, and the two int8 pieces relative to sigma_g =

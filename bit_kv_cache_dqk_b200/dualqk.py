@@ -26,7 +26,10 @@ DQK_F32, DQK_BF16 = 0, 1
 EXPORTED = ["dqk_block_bytes", "dqk_append", "dqk_decode_workspace_size", "dqk_decode",
             "dqk_decode_step", "dqk_decode_partial", "dqk_merge_partials", "dqk_test_decode_stall",
             "dqk_decode_noalloc", "dqk_bf16_block_bytes", "dqk_bf16_append",
-            "dqk_bf16_decode_workspace_size", "dqk_bf16_decode", "dqk_last_device_error", "dqk_status_string"]
+            "dqk_bf16_decode_workspace_size", "dqk_bf16_decode", "dqk_rope_append", "dqk_bf16_rope_append",
+            "dqk_prefix_decode_workspace_size", "dqk_prefix_decode", "dqk_bf16_prefix_decode_workspace_size",
+            "dqk_bf16_prefix_decode", "dqk_bf16_cross_attention_workspace_size", "dqk_bf16_cross_attention",
+            "dqk_last_device_error", "dqk_status_string"]
 
 DQK_NOALLOC_WORKSPACE_BYTES = 8 << 20
 
@@ -38,7 +41,13 @@ class dqk_layer_desc(C.Structure):
                 ("num_pages", C.c_longlong)]
 
 
+class dqk_rope_desc(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int), ("interleaved", C.c_int), ("cos_sin", C.c_void_p),
+                ("max_position", C.c_longlong)]
+
+
 _P = C.c_void_p
+_R = C.POINTER(dqk_rope_desc)
 _D = C.POINTER(dqk_layer_desc)
 _lib.dqk_block_bytes.restype = C.c_size_t
 _lib.dqk_block_bytes.argtypes = [_D]
@@ -65,6 +74,24 @@ _lib.dqk_bf16_decode_workspace_size.restype = C.c_size_t
 _lib.dqk_bf16_decode_workspace_size.argtypes = [_D, C.c_int, C.c_int]
 _lib.dqk_bf16_decode.restype = C.c_int
 _lib.dqk_bf16_decode.argtypes = [_D, _P, C.c_int, C.c_int, _P, _P, C.c_int, _P, _P, C.c_size_t, _P]
+for _n in ("dqk_rope_append", "dqk_bf16_rope_append"):
+    getattr(_lib, _n).restype = C.c_int
+    getattr(_lib, _n).argtypes = [_D, _R, _P, C.c_longlong, _P, C.c_longlong, _P, C.c_longlong, _P, C.c_longlong,
+                                  C.c_int, C.c_int, _P, _P, C.c_int, _P, _P, C.c_int, _P]
+for _n in ("dqk_prefix_decode_workspace_size", "dqk_bf16_prefix_decode_workspace_size"):
+    getattr(_lib, _n).restype = C.c_size_t
+    getattr(_lib, _n).argtypes = [_D, C.c_int, C.c_int, C.c_int, C.c_int]
+_lib.dqk_prefix_decode.restype = C.c_int
+_lib.dqk_prefix_decode.argtypes = [_D, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, C.c_int, _P, _P, C.c_int, C.c_int,
+                                   _P, C.c_int, _P, _P, C.c_size_t, _P]
+_lib.dqk_bf16_prefix_decode.restype = C.c_int
+_lib.dqk_bf16_prefix_decode.argtypes = [_D, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, C.c_int, _P, _P, C.c_int, _P,
+                                        C.c_int, _P, C.c_size_t, _P]
+_lib.dqk_bf16_cross_attention_workspace_size.restype = C.c_size_t
+_lib.dqk_bf16_cross_attention_workspace_size.argtypes = [_D, C.c_int, C.c_int, C.c_int]
+_lib.dqk_bf16_cross_attention.restype = C.c_int
+_lib.dqk_bf16_cross_attention.argtypes = [_D, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, C.c_int, _P, C.c_int, _P,
+                                          C.c_size_t, _P]
 _lib.dqk_last_device_error.restype = C.c_int
 _lib.dqk_last_device_error.argtypes = [_P]
 _lib.dqk_status_string.restype = C.c_char_p
@@ -104,6 +131,10 @@ def layer_desc(head_dim, num_q_heads, num_kv_heads, t_k, t_q, pool, num_pages, v
                page_size=16, group_size=32) -> dqk_layer_desc:
     return dqk_layer_desc(head_dim, num_q_heads, num_kv_heads, page_size, group_size, v_ch0_protect,
                           _addr(t_k), _addr(t_q), _addr(pool), num_pages)
+
+
+def rope_desc(rotary_dim, cos_sin, max_position, interleaved=0) -> dqk_rope_desc:
+    return dqk_rope_desc(rotary_dim, interleaved, _addr(cos_sin), max_position)
 
 
 def dqk_block_bytes(layer: dqk_layer_desc) -> int:
@@ -193,6 +224,76 @@ def dqk_bf16_decode(layer, q, q_dtype, batch, seq_lens, page_table, max_pages, o
     st = _lib.dqk_bf16_decode(C.byref(layer), _addr(q), q_dtype, batch, _addr(seq_lens), _addr(page_table),
                               max_pages, _addr(out), _addr(workspace), workspace_bytes, _stream(stream))
     return _check(st, "dqk_bf16_decode", raise_on_error)
+
+
+def _rope_append(fn, name, layer, rope, k, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, dtype, batch,
+                 new_lens, seq_lens_before, max_new, positions, page_table, max_pages, stream, raise_on_error):
+    st = fn(C.byref(layer), C.byref(rope), _addr(k), k_stride, _addr(v), v_stride, _addr(q), q_stride, _addr(q_out),
+            q_out_stride, dtype, batch, _addr(new_lens), _addr(seq_lens_before), max_new, _addr(positions),
+            _addr(page_table), max_pages, _stream(stream))
+    return _check(st, name, raise_on_error)
+
+
+def dqk_rope_append(layer, rope, k, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, dtype, batch, new_lens,
+                    seq_lens_before, max_new, positions, page_table, max_pages, stream=None, raise_on_error=True) -> int:
+    """Rotary embedding, INT2 cache append and query rotation in one launch
+    (strides in elements; see include/dualqk.h)."""
+    return _rope_append(_lib.dqk_rope_append, "dqk_rope_append", layer, rope, k, k_stride, v, v_stride, q, q_stride,
+                        q_out, q_out_stride, dtype, batch, new_lens, seq_lens_before, max_new, positions, page_table,
+                        max_pages, stream, raise_on_error)
+
+
+def dqk_bf16_rope_append(layer, rope, k, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, dtype, batch,
+                         new_lens, seq_lens_before, max_new, positions, page_table, max_pages, stream=None,
+                         raise_on_error=True) -> int:
+    return _rope_append(_lib.dqk_bf16_rope_append, "dqk_bf16_rope_append", layer, rope, k, k_stride, v, v_stride, q,
+                        q_stride, q_out, q_out_stride, dtype, batch, new_lens, seq_lens_before, max_new, positions,
+                        page_table, max_pages, stream, raise_on_error)
+
+
+def dqk_prefix_decode_workspace_size(layer, batch, n_prefixes, max_prefix_pages, max_pages) -> int:
+    return int(_lib.dqk_prefix_decode_workspace_size(C.byref(layer), batch, n_prefixes, max_prefix_pages, max_pages))
+
+
+def dqk_prefix_decode(layer, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table, max_prefix_pages,
+                      seq_lens, page_table, max_pages, sparsity_pct, out, out_dtype, sel_out, workspace,
+                      workspace_bytes, stream=None, raise_on_error=True) -> int:
+    """Decode of a batch behind shared prefixes, each prefix read once (INT2
+    cache; see include/dualqk.h)."""
+    st = _lib.dqk_prefix_decode(C.byref(layer), _addr(q), q_dtype, batch, n_prefixes, _addr(prefix_start),
+                                _addr(prefix_lens), _addr(prefix_table), max_prefix_pages, _addr(seq_lens),
+                                _addr(page_table), max_pages, sparsity_pct, _addr(out), out_dtype, _addr(sel_out),
+                                _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "dqk_prefix_decode", raise_on_error)
+
+
+def dqk_bf16_prefix_decode_workspace_size(layer, batch, n_prefixes, max_prefix_pages, max_pages) -> int:
+    return int(_lib.dqk_bf16_prefix_decode_workspace_size(C.byref(layer), batch, n_prefixes, max_prefix_pages,
+                                                          max_pages))
+
+
+def dqk_bf16_prefix_decode(layer, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
+                           max_prefix_pages, seq_lens, page_table, max_pages, out, out_dtype, workspace,
+                           workspace_bytes, stream=None, raise_on_error=True) -> int:
+    st = _lib.dqk_bf16_prefix_decode(C.byref(layer), _addr(q), q_dtype, batch, n_prefixes, _addr(prefix_start),
+                                     _addr(prefix_lens), _addr(prefix_table), max_prefix_pages, _addr(seq_lens),
+                                     _addr(page_table), max_pages, _addr(out), out_dtype, _addr(workspace),
+                                     workspace_bytes, _stream(stream))
+    return _check(st, "dqk_bf16_prefix_decode", raise_on_error)
+
+
+def dqk_bf16_cross_attention_workspace_size(layer, batch, total_q, max_pages) -> int:
+    return int(_lib.dqk_bf16_cross_attention_workspace_size(C.byref(layer), batch, total_q, max_pages))
+
+
+def dqk_bf16_cross_attention(layer, q, q_dtype, batch, total_q, q_start, kv_lens, page_table, max_pages, out,
+                             out_dtype, workspace, workspace_bytes, stream=None, raise_on_error=True) -> int:
+    """Query rows of each sequence against its encoder states in the BF16 cache
+    (see include/dualqk.h)."""
+    st = _lib.dqk_bf16_cross_attention(C.byref(layer), _addr(q), q_dtype, batch, total_q, _addr(q_start),
+                                       _addr(kv_lens), _addr(page_table), max_pages, _addr(out), out_dtype,
+                                       _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "dqk_bf16_cross_attention", raise_on_error)
 
 
 def dqk_last_device_error(stream=None) -> int:

@@ -298,6 +298,122 @@ dqk_status dqk_bf16_decode(const dqk_layer_desc *layer, const void *q, dqk_dtype
                            const int *seq_lens, const int *page_table, int max_pages, float *out,
                            void *workspace, size_t workspace_bytes, dqk_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Appends with the rotary position embedding applied on the way, and the
+ * queries of the same rows rotated by the same angles.  (The pages put RoPE
+ * before the key transform; dqk_append leaves rotating to the caller.)
+ *
+ *  rotary_dim    r: channels 0..r-1 are rotated, the others pass; a multiple
+ *                of 16, at most head_dim.
+ *  interleaved   0: pairs (i, i + r/2); 1: pairs (2i, 2i + 1); i < r/2.
+ *  cos_sin       (device) fp32 [max_position][r]: the cosines of the r/2 pairs
+ *                of a position, then their sines.  16-byte aligned.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int rotary_dim;
+    int interleaved;
+    const float *cos_sin;
+    long long max_position;
+} dqk_rope_desc;
+
+/* dqk_rope_append -- dqk_append of rotated keys (INT2 cache): per pair
+ * (a, b) -> (a c - b s, b c + a s), then k' = T_K k and the quantizer.
+ *  k, v          (device) rows of [Hkv][d], k_stride / v_stride elements apart
+ *                (at least Hkv * d; slices of a fused projection's rows will
+ *                do), sequence b's rows after those of b-1.
+ *  q, q_out      (device, both or neither null) rows of [Hq][d] of the same
+ *                tokens, q_stride / q_out_stride elements apart; q_out gets
+ *                the rotated queries in `dtype`.  q_out may be q itself (same
+ *                stride); otherwise the two must not overlap.
+ *  dtype         of k, v, q and q_out.  Pointers 16-byte aligned, strides a
+ *                multiple of 16 bytes.
+ *  positions     (device, nullable) int [sum(new_lens)]: the position of each
+ *                new row (behind a shared prefix it is not the cache slot);
+ *                null: seq_lens_before[b] + t.
+ *  The others as in dqk_append.
+ * The rotated key is formed in fp64 (exact products) and rounded to fp32; the
+ * codes that follow have the one value dqk_append's definition gives for it.
+ * Queries are rotated in fp32 and rounded once to `dtype`.  A row whose page
+ * or position is out of range is skipped -- key, value and query -- and sets
+ * the device error word; so do rows past max_new. */
+dqk_status dqk_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc *rope, const void *k, long long k_stride,
+                           const void *v, long long v_stride, const void *q, long long q_stride, void *q_out,
+                           long long q_out_stride, dqk_dtype dtype, int batch, const int *new_lens,
+                           const int *seq_lens_before, int max_new, const int *positions, const int *page_table,
+                           int max_pages, dqk_stream_t stream);
+
+/* The same into the BF16 cache: keys rotated in fp32, keys and values rounded
+ * to BF16 (RNE). */
+dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc *rope, const void *k,
+                                long long k_stride, const void *v, long long v_stride, const void *q,
+                                long long q_stride, void *q_out, long long q_out_stride, dqk_dtype dtype, int batch,
+                                const int *new_lens, const int *seq_lens_before, int max_new, const int *positions,
+                                const int *page_table, int max_pages, dqk_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode of a batch that shares long prefixes: every sequence attends its
+ * prefix's tokens and then its own, and a prefix is read once for all its
+ * sequences.  (dqk_decode over a page table that repeats the prefix's pages
+ * gives the same attention and reads them once per sequence.)
+ *
+ *  q                (device) [batch][Hq][d], 16-byte aligned, RoPE applied.
+ *  prefix_start     (device) int [n_prefixes + 1], ascending: sequences
+ *                   prefix_start[g] .. prefix_start[g+1]-1 share prefix g.  A
+ *                   sequence in no group has its own tokens only.
+ *  prefix_lens      (device) int [n_prefixes]: tokens of each prefix (0: none).
+ *  prefix_table     (device) int [n_prefixes][max_prefix_pages].
+ *  seq_lens, page_table, max_pages  each sequence's own tokens, as in
+ *                   dqk_decode; max_pages 0 (both may be null): none.
+ *  out              (device) [batch][Hq][d] in out_dtype, 16-byte aligned; 0
+ *                   for a sequence without any token.
+ *  workspace        (device) at least the workspace size, 256-byte aligned;
+ *                   scratch, no initialisation.
+ * Lengths beyond a page table's reach are cut to it, bad page ids skipped, and
+ * both set the device error word.
+ *
+ * dqk_prefix_decode (INT2 cache): T_Q, sparsity_pct and sel_out as in
+ * dqk_decode, with the same kept channels; T_Q 16-byte aligned.  Scores and
+ * values use fp16 operands (queries scaled per row, 2^-11 per kept channel;
+ * k^ and v^ rounded once, 2^-11; weights 2^-11) with fp32 accumulation:
+ * dequantized magnitudes above fp16's 65504 are outside its range.
+ * dqk_bf16_prefix_decode (BF16 cache): fp32 queries are carried as BF16 high +
+ * low parts, softmax weights in BF16 (2^-8), accumulation in fp32.
+ * ------------------------------------------------------------------------- */
+size_t dqk_prefix_decode_workspace_size(const dqk_layer_desc *layer, int batch, int n_prefixes, int max_prefix_pages,
+                                        int max_pages);
+dqk_status dqk_prefix_decode(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch, int n_prefixes,
+                             const int *prefix_start, const int *prefix_lens, const int *prefix_table,
+                             int max_prefix_pages, const int *seq_lens, const int *page_table, int max_pages,
+                             int sparsity_pct, void *out, dqk_dtype out_dtype, int16_t *sel_out, void *workspace,
+                             size_t workspace_bytes, dqk_stream_t stream);
+
+size_t dqk_bf16_prefix_decode_workspace_size(const dqk_layer_desc *layer, int batch, int n_prefixes,
+                                             int max_prefix_pages, int max_pages);
+dqk_status dqk_bf16_prefix_decode(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch,
+                                  int n_prefixes, const int *prefix_start, const int *prefix_lens,
+                                  const int *prefix_table, int max_prefix_pages, const int *seq_lens,
+                                  const int *page_table, int max_pages, void *out, dqk_dtype out_dtype, void *workspace,
+                                  size_t workspace_bytes, dqk_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * dqk_bf16_cross_attention -- any number of query tokens per sequence against
+ * that sequence's encoder states in the BF16 cache (filled by dqk_bf16_append),
+ * no causal mask:  out_r = softmax(q_r . k_t / sqrt(d)) . v_t over t < kv_lens[b].
+ *  q             (device) [total_q][Hq][d], 16-byte aligned.
+ *  q_start       (device) int [batch + 1], ascending: rows q_start[b] ..
+ *                q_start[b+1]-1 of q belong to sequence b (none: equal bounds).
+ *                Rows of no sequence are left as they were in out.
+ *  kv_lens       (device) int [batch]; 0 gives zero rows.
+ *  page_table    (device) int [batch][max_pages].
+ *  out           (device) [total_q][Hq][d] in out_dtype, 16-byte aligned.
+ *  Precision and errors as in dqk_bf16_prefix_decode.
+ * ------------------------------------------------------------------------- */
+size_t dqk_bf16_cross_attention_workspace_size(const dqk_layer_desc *layer, int batch, int total_q, int max_pages);
+dqk_status dqk_bf16_cross_attention(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch,
+                                    int total_q, const int *q_start, const int *kv_lens, const int *page_table,
+                                    int max_pages, void *out, dqk_dtype out_dtype, void *workspace,
+                                    size_t workspace_bytes, dqk_stream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the current device's error
  * word: DQK_OK, DQK_ERR_DEVICE_BOUNDS or DQK_ERR_TIMEOUT (DQK_ERR_CUDA if the
  * stream itself reports an error).  All calls on a device share the word. */
