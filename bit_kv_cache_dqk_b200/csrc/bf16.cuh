@@ -52,10 +52,11 @@ __global__ void __launch_bounds__(2 * D / 8) k_append_b16(const void *__restrict
         if (threadIdx.x == 0) dqk_flag_error(kErrBounds);
         return;
     }
+    constexpr int kLanes = 2 * kChunks < 32 ? 2 * kChunks : 32;   // threads of a warp of this block (16 with head_dim 64)
     int row0 = 0;
-    for (int bb = threadIdx.x & 31; bb < b; bb += 32) row0 += new_lens[bb];
+    for (int bb = threadIdx.x % kLanes; bb < b; bb += kLanes) row0 += new_lens[bb];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) row0 += __shfl_xor_sync(0xffffffffu, row0, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) row0 += __shfl_xor_sync(kLanes == 32 ? 0xffffffffu : 0xffffu, row0, o);
     const int is_v = threadIdx.x / kChunks, x = threadIdx.x % kChunks;
     const size_t src = (((size_t)row0 + t) * hkv + j) * D + 8 * x;
     const void *in = is_v ? vin : kin;

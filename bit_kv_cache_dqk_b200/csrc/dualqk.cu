@@ -898,9 +898,9 @@ namespace {
 // Workspace: [query rows fp16 | their scales | group records | own records],
 // sections 256-byte aligned.
 struct RowsPlanHost {
-    int d, G, stages, bb;
-    long long slots, own_slots;
-    size_t off_scale, off_rec, off_own, bytes, smem;
+    int d, G, bb;
+    long long slots, own_slots, tiles;
+    size_t off_scale, off_rec, off_own, bytes;
     long long max_units;
 };
 
@@ -911,23 +911,50 @@ bool plan_rows(const dqk_layer_desc *L, bool int2, int total_rows, int n_groups,
     const long long hkv = L->num_kv_heads;
     if ((long long)total_rows * L->num_q_heads >= (1LL << 31) / 2) return false;
     if (((long long)max_pages + own_pages) * kPage >= (1LL << 31)) return false;
-    const long long tiles = n_groups + (long long)total_rows * P.G / kRowsTile;   // >= the groups' row tiles
-    if (tiles * hkv >= (1LL << 31) / 2 || (long long)n_own * hkv >= (1LL << 31) / 2) return false;
-    P.slots = kMaxAttendCtas + tiles * hkv;
+    if (L->num_pages * hkv >= (1LL << 31)) return false;   // block numbers are tensor-copy coordinates
+    P.tiles = n_groups + (long long)total_rows * P.G / kRowsTile;   // >= the groups' row tiles
+    if (P.tiles * hkv >= (1LL << 31) / 2 || (long long)n_own * hkv >= (1LL << 31) / 2) return false;
+    P.slots = n_own ? kMaxAttendCtas + P.tiles * hkv : 2 * kMaxAttendCtas;   // rows_slot
     P.own_slots = n_own ? kMaxAttendCtas + n_own * hkv : 0;
-    P.max_units = hkv * (tiles * ((max_pages + kRowsPages - 1) / kRowsPages) +
+    P.max_units = hkv * (2 * P.tiles * ((max_pages + kRowsPages - 1) / kRowsPages) +
                          (long long)n_own * ((own_pages + kRowsPages - 1) / kRowsPages));
     P.bb = int2 ? make_layout(P.d, L->v_ch0_protect, P.d / L->group_size).bytes : b16_block_bytes(P.d);
-    const size_t stage = (size_t)kRowsPages * P.bb;
-    P.stages = (int)std::min<size_t>(kMaxStages, (227 * 1024 - kRowsFixedSmem) / stage);
-    P.smem = P.stages * stage + kRowsFixedSmem;
     const size_t heads = (size_t)total_rows * L->num_q_heads;
     P.off_scale = int2 ? round_up(heads * P.d * 2, 256) : 0;
     P.off_rec = P.off_scale + (int2 ? round_up(heads * sizeof(float), 256) : 0);
     const size_t row = rec_stride(P.d) * sizeof(float);
-    P.off_own = P.off_rec + round_up((size_t)P.slots * kRowsTile * row, 256);
-    P.bytes = P.off_own + round_up((size_t)P.own_slots * kRowsWarps * P.G * row, 256);
+    P.off_own = P.off_rec + round_up((size_t)P.slots * 2 * kRowsHalf * row, 256);
+    P.bytes = P.off_own + round_up((size_t)P.own_slots * 2 * P.G * row, 256);
     return true;
+}
+
+// The BF16 pool as a tensor of 16-bit elements [block][column block of 64][32 token rows, K then V][64]:
+// one box is one page's 16 keys or values.
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+dqk_status pool_map(const dqk_layer_desc *L, CUtensorMap &map) {
+    static std::atomic<EncodeTiled> fn{nullptr};
+    EncodeTiled encode = fn.load(std::memory_order_acquire);
+    if (!encode) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !f)
+            return DQK_ERR_CUDA;
+        encode = reinterpret_cast<EncodeTiled>(f);
+        fn.store(encode, std::memory_order_release);
+    }
+    const cuuint64_t d = (cuuint64_t)L->head_dim;
+    const cuuint64_t dims[4] = {64, 2 * kPage, d / 64, (cuuint64_t)(L->num_pages * L->num_kv_heads)};
+    const cuuint64_t strides[3] = {2 * d, 128, (cuuint64_t)b16_block_bytes(L->head_dim)};
+    const cuuint32_t box[4] = {64, kPage, (cuuint32_t)(d / 64), 1}, one[4] = {1, 1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, L->pool, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                   CUDA_SUCCESS
+               ? DQK_OK
+               : DQK_ERR_CUDA;
 }
 
 // Launch with programmatic stream serialization: the kernel may start while the
@@ -969,14 +996,36 @@ struct RowsCall {
 };
 
 template <int D, int kFmt, int NS, bool VCH0>
-dqk_status run_rows_kernels(const RowsParams &p, const RowsPlanHost &P, int dev, cudaStream_t stream) {
-    dqk_status st = prepare_kernel<k_rows<D, kFmt, NS, VCH0>>(dev, P.smem, kRowsThreads);
+dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost &P, int dev) {
+    using T = RowsShape<D, kFmt>;
+    // shared memory: 1024 bytes of alignment, the query tiles, the rings
+    constexpr size_t kBudget = 227 * 1024 - 1024 - sizeof(RowsBars) - 2 * T::kParts * T::kTile;
+    // a key tile is free again as soon as its scores are formed, a value tile only after its unit's weights: with an
+    // odd number the values have one more
+    const int tiles = T::kInt2 ? 4 : (int)std::min<size_t>(kRowsMaxTiles, kBudget / T::kTile);
+    p.ktiles = tiles / 2;
+    p.vtiles = tiles - p.ktiles;
+    // page flags: at most kRowsFlags units between their copies and the softmax
+    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kBudget - 4 * T::kTile) / (kRowsPages * P.bb)) : 0;
+    const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb;
+    dqk_status st = prepare_kernel<k_rows<D, kFmt, NS, VCH0>>(dev, smem, T::kThreads);
     if (st != DQK_OK) return st;
-    st = launch_overlapped(k_rows<D, kFmt, NS, VCH0>, dim3(p.num_ctas), kRowsThreads, P.smem, stream, p);
+    CUtensorMap map = {};
+    if (!T::kInt2) {
+        st = pool_map(a.layer, map);
+        if (st != DQK_OK) return st;
+    }
+    st = launch_overlapped(k_rows<D, kFmt, NS, VCH0>, dim3(p.num_ctas), T::kThreads, smem, a.stream, p, map);
     if (st != DQK_OK) return st;
-    const long long heads = (long long)p.total_rows * p.hq;
-    return launch_overlapped(k_rows_merge<D>, dim3((unsigned)((heads + kRowsMergeWarps - 1) / kRowsMergeWarps)),
-                             32 * kRowsMergeWarps, 0, stream, p);
+    if (p.n_own > 0) {
+        const int warps = std::min(p.hq, kRowsMergeHeads);
+        return launch_overlapped(k_rows_merge<D>, dim3((unsigned)p.total_rows, (p.hq + warps - 1) / warps), 32 * warps, 0,
+                                 a.stream, p);
+    }
+    const int rows = (int)std::min<long long>(kRowsTile, (long long)p.total_rows * p.G);
+    return launch_overlapped(k_rows_merge_items<D>,
+                             dim3((unsigned)(p.num_ctas - 1 + std::min(p.n_groups, 32)), (rows + kRowsMergeRows - 1) / kRowsMergeRows),
+                             32 * kRowsMergeWarps, 0, a.stream, p);
 }
 
 // the INT2 cache: transformed and pruned fp16 query rows first
@@ -992,8 +1041,8 @@ dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint1
 template <int D>
 dqk_status run_rows_d(const RowsCall &a, const RowsPlanHost &P, RowsParams &p, int dev) {
     if (!a.int2) {
-        return a.q_dtype == DQK_BF16 ? run_rows_kernels<D, 0, 1, false>(p, P, dev, a.stream)
-                                     : run_rows_kernels<D, 1, 1, false>(p, P, dev, a.stream);
+        return a.q_dtype == DQK_BF16 ? run_rows_kernels<D, 0, 1, false>(a, p, P, dev)
+                                     : run_rows_kernels<D, 1, 1, false>(a, p, P, dev);
     }
     char *ws = static_cast<char *>(a.ws);
     uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
@@ -1006,10 +1055,10 @@ dqk_status run_rows_d(const RowsCall &a, const RowsPlanHost &P, RowsParams &p, i
     p.q = rows;
     p.q_scale = scale;
     const bool one = a.layer->group_size == D, v0 = a.layer->v_ch0_protect != 0;
-    if (one) return v0 ? run_rows_kernels<D, 2, 1, true>(p, P, dev, a.stream)
-                       : run_rows_kernels<D, 2, 1, false>(p, P, dev, a.stream);
-    return v0 ? run_rows_kernels<D, 2, D / kGroup, true>(p, P, dev, a.stream)
-              : run_rows_kernels<D, 2, D / kGroup, false>(p, P, dev, a.stream);
+    if (one) return v0 ? run_rows_kernels<D, 2, 1, true>(a, p, P, dev)
+                       : run_rows_kernels<D, 2, 1, false>(a, p, P, dev);
+    return v0 ? run_rows_kernels<D, 2, D / kGroup, true>(a, p, P, dev)
+              : run_rows_kernels<D, 2, D / kGroup, false>(a, p, P, dev);
 }
 
 dqk_status run_rows(const RowsCall &a) {
@@ -1039,7 +1088,6 @@ dqk_status run_rows(const RowsCall &a) {
     p.own_table = a.own_table;
     p.own_max_pages = a.own_pages;
     p.q = a.q;
-    p.q_dtype = (int)a.q_dtype;
     p.qs = (float)(1.4426950408889634 / std::sqrt((double)P.d));
     char *ws = static_cast<char *>(a.ws);
     p.rec = reinterpret_cast<float *>(ws + P.off_rec);
@@ -1051,7 +1099,6 @@ dqk_status run_rows(const RowsCall &a) {
     p.hkv = L->num_kv_heads;
     p.G = P.G;
     p.bb = P.bb;
-    p.stages = P.stages;
     p.num_ctas = (int)std::max<long long>(1, std::min<long long>(std::min(sms, kMaxAttendCtas), P.max_units));
     p.wait_ns = kRingWaitNs;
     return P.d == 128 ? run_rows_d<128>(a, P, p, dev) : run_rows_d<64>(a, P, p, dev);

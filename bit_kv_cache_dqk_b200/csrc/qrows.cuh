@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "ptx.cuh"
 #include "qprep.cuh"
+#include "rows.cuh"
 
 namespace dqk {
 
@@ -19,7 +20,8 @@ template <int D, int G>
 __host__ __device__ constexpr int query_rows_threads() { return 32 * (D / 32 > G ? D / 32 : G); }
 
 // CTA per (query row, kv head).  Row head (row, h) becomes
-//   qr [row][hq][D] fp16 = rne(2^k q'_c) on the kept channels, 0 elsewhere, with
+//   qr [row][hq][D] fp16 = rne(2^k q'_c) on the kept channels, 0 elsewhere, in the
+//   channel order of the key operand tiles (rows_channel_pos), with
 //   k such that the largest kept |q'_c| lies in [2^14, 2^15): fp16's 11 bits then
 //   cover channels down to 2^-28 of it;
 //   scale [row][hq] = 2^-k log2(e)/sqrt(d), which the scores are multiplied by.
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(query_rows_threads<D, G>()) k_query_rows(
     const int k = e == 0 || e == 255 ? 0 : 14 - (e - 127);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        qr[at * D + lane + 32 * g] = __half_as_ushort(__float2half_rn(ldexpf(v[g], k)));
+        qr[at * D + rows_channel_pos(lane + 32 * g)] = __half_as_ushort(__float2half_rn(ldexpf(v[g], k)));
     if (lane == 0) scale[at] = ldexpf(qscale, -k);
 }
 

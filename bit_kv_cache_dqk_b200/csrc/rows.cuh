@@ -8,14 +8,34 @@
 // row counts G times (its G query heads), so a group of n rows is a matrix of
 // n G "row heads" against the list's tokens:
 //   S = Q K^T,  P = 2^(S qs - m),  O = P V,   qs = log2(e)/sqrt(d)
-// with the running maximum m and sum l per row head (online softmax), split
-// over the tokens into records (m, l, o) that k_rows_merge joins.
+// with a reference m and the sum l of P per row head (online softmax).
 //
-// Work split: item = (group, tile of 128 row heads, kv head), then (own list,
-// kv head); unit = kRowsKv tokens of an item.  CTA c of C takes units
-// [floor(cU/C), floor((c+1)U/C)), so the CTAs stream the same number of tokens
-// whatever the lengths.
+// Work split: item = (group, tile of 256 row heads, kv head), then (own list,
+// kv head); unit = 128 tokens of an item.  A unit of a tile of more than 128
+// row heads weighs 2, others 1; CTA c takes the units that start in
+// [cq, (c+1)q) of all U weighted units, q = ceil(U / C), so every CTA does
+// about the same work whatever the lengths.
+//
+// One CTA per SM, warp-specialized around the tensor core (tcgen05, operands in
+// shared memory and TMEM, fp32 accumulators in TMEM):
+//   producer warp   brings the pages in (BF16: tensor copies that leave each
+//                   128-byte half row in the 128-byte-swizzled operand layout
+//                   the block format already is; INT2: 1-D bulk copies of the
+//                   packed blocks),
+//   unpack warps    (INT2) turn packed blocks into fp16 operand tiles,
+//   two softmax warpgroups, one row head per thread,
+//   two matrix threads, one per warpgroup, which issue S = Q K^T and O += P V.
+// The jobs of a CTA -- (unit, 128 row heads) -- go to the two warpgroups in
+// turn: a tile of more than 128 row heads gives each unit to both, its halves;
+// a smaller tile gives the units to one and the other, each with its own
+// reference, sum and accumulator.  A job goes through in two halves of 64 tokens --
+// half h: tokens 8h .. 8h + 7 of every page, in page order -- each with its own 64
+// columns of TMEM for S and then P: while a warpgroup turns one
+// half's scores into weights, the tensor core takes the other half's weights and
+// forms the next job's scores.
 #pragma once
+
+#include <cuda.h>
 
 #include "attend.cuh"
 #include "common.cuh"
@@ -23,12 +43,18 @@
 
 namespace dqk {
 
-constexpr int kRowsTile = 128;                    // row heads of an item
+constexpr int kRowsTile = 256;                    // row heads of an item
+constexpr int kRowsHalf = 128;                    // row heads of a job
 constexpr int kRowsKv = 128;                      // tokens of a unit
 constexpr int kRowsPages = kRowsKv / kPage;       // pages of a unit
-constexpr int kRowsWarps = 8;                     // consumer warps
-constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
-constexpr float kRowsPScale = 16384.0f;           // softmax weights in fp16 are carried times 2^14
+constexpr int kRowsUnpackWarps = 4;
+constexpr int kRowsFlags = 8;                     // units in flight at most (page flags)
+// fp16 weights (INT2) are carried times 2^6, and so is their sum (the factor leaves with it): a
+// weight is at most 2^8 (see kRowsSlack), so 2^14 at most, and keeps 11 bits down to 2^-20.
+constexpr float kRowsLift = 6.0f;
+// The reference m moves only when a score passes it by more than this (log2 units): weights
+// are then at most 2^8 and the accumulator is rescaled a few times per item at most.
+constexpr float kRowsSlack = 8.0f;
 
 struct RowsParams {
     const uint8_t *pool;
@@ -41,17 +67,16 @@ struct RowsParams {
     int n_own;
     const int *own_lens, *own_table;
     int own_max_pages;
-    // queries: BF16 cache, the caller's rows [total_rows][hq][D] (q_dtype);
-    // INT2 cache, prepared fp16 rows and their scales (k_query_rows)
+    // queries: BF16 cache, the caller's rows [total_rows][hq][D]; INT2 cache,
+    // prepared fp16 rows and their scales (k_query_rows)
     const void *q;
-    int q_dtype;
     const float *q_scale;
     float qs;
     float *rec, *own_rec;       // split records of the groups' and of the own items
     long long rec_slots;        // slots `rec` holds (row_start out of order could ask for more)
     void *out;
     int out_dtype;
-    int hq, hkv, G, bb, stages, num_ctas;
+    int hq, hkv, G, bb, ktiles, vtiles, raw_stages, num_ctas;
     unsigned long long wait_ns;
 };
 
@@ -67,9 +92,26 @@ __device__ __forceinline__ int rows_units(int len) { return (int)(((long long)le
 __device__ __forceinline__ int rows_first(const RowsParams &p, int g) {
     return min(max(p.row_start[g], 0), p.total_rows);
 }
-__device__ __forceinline__ int rows_tiles(const RowsParams &p, int g) {
-    const int n = rows_first(p, g + 1) - rows_first(p, g);
-    return n > 0 ? (int)(((long long)n * p.G + kRowsTile - 1) / kRowsTile) : 0;
+
+// A list's shape: row tiles (the last one's weight), units of a tile, weighted units in all.
+struct RowsList {
+    int tiles, last, per;
+    long long units;
+};
+__device__ __forceinline__ RowsList rows_list(const RowsParams &p, int i) {
+    RowsList r;
+    if (i < p.n_groups) {
+        const int n = max(rows_first(p, i + 1) - rows_first(p, i), 0) * p.G;
+        r.tiles = (n + kRowsTile - 1) / kRowsTile;
+        r.last = n - (r.tiles - 1) * kRowsTile > kRowsHalf ? 2 : 1;
+        r.per = rows_units(rows_len(p.kv_lens, i, p.max_pages));
+    } else {
+        r.tiles = 1;
+        r.last = 1;
+        r.per = rows_units(rows_len(p.own_lens, i - p.n_groups, p.own_max_pages));
+    }
+    r.units = r.tiles ? (long long)p.hkv * r.per * (2 * (r.tiles - 1) + r.last) : 0;
+    return r;
 }
 
 // Inclusive prefix sum over a warp.
@@ -82,14 +124,13 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
     return x;
 }
 
-// Units and row tiles of the groups before g (g = n_groups: all); warp-collective.
-__device__ __forceinline__ void rows_before_group(const RowsParams &p, int g, int lane, long long &units,
-                                                  long long &tiles) {
+// Weighted units and row tiles of the lists before list n; warp-collective.
+__device__ __forceinline__ void rows_sums(const RowsParams &p, int n, int lane, long long &units, long long &tiles) {
     long long u = 0, t = 0;
-    for (int i = lane; i < g; i += 32) {
-        const int nt = rows_tiles(p, i);
-        t += nt;
-        u += (long long)nt * p.hkv * rows_units(rows_len(p.kv_lens, i, p.max_pages));
+    for (int i = lane; i < n; i += 32) {
+        const RowsList r = rows_list(p, i);
+        u += r.units;
+        t += i < p.n_groups ? r.tiles : 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -99,122 +140,224 @@ __device__ __forceinline__ void rows_before_group(const RowsParams &p, int g, in
     units = u;
     tiles = t;
 }
-// Units of the own lists before b.
-__device__ __forceinline__ long long rows_before_own(const RowsParams &p, int b, int lane) {
-    long long u = 0;
-    for (int i = lane; i < b; i += 32) u += (long long)p.hkv * rows_units(rows_len(p.own_lens, i, p.own_max_pages));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    return u;
-}
 
-// The CTA's units [u0, u1) of U (U_g of them the groups'), and the list that holds u0.
-struct RowsPlan {
-    long long U, Ug, u0, u1;
-    long long first_unit;   // first unit of that list
-    long long first_tile;   // row tiles of the groups before it
-    int list;               // group index, or n_groups + own index
+// Walks the segments -- stretches of one item's units -- of a CTA in order.
+struct RowsCursor {
+    long long u0, u1;       // the CTA's weighted units
+    long long first;        // first weighted unit of the list
+    long long tile0;        // row tiles of the groups before it
+    int list, k;            // list, next (tile, kv head) of it
 };
 
-__device__ __forceinline__ RowsPlan rows_plan(const RowsParams &p, int cta, int num_ctas, int lane) {
-    RowsPlan r;
-    long long nt;
-    rows_before_group(p, p.n_groups, lane, r.Ug, nt);
-    r.U = r.Ug + rows_before_own(p, p.n_own, lane);
-    r.u0 = (long long)cta * r.U / num_ctas;
-    r.u1 = ((long long)cta + 1) * r.U / num_ctas;
-    r.list = p.n_groups + p.n_own;
-    r.first_unit = r.U;
-    r.first_tile = nt;
-    long long base = 0, tbase = 0;
-    for (int i0 = 0; i0 < p.n_groups + p.n_own; i0 += 32) {
+// Weighted units per CTA (and the general quotient: 32-bit division where it fits).
+__device__ __forceinline__ long long rows_div(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+__device__ __forceinline__ long long rows_share(long long U, int ctas) { return max(rows_div(U + ctas - 1, ctas), 1LL); }
+
+// The CTA's cursor at its first list; warp-collective.
+__device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, int lane) {
+    const int n = p.n_groups + p.n_own;
+    // one pass when every list has a lane, else the sums first
+    long long U = 0, tiles = 0, base = 0, tbase = 0;
+    if (n > 32) rows_sums(p, n, lane, U, tiles);
+    RowsCursor c{0, 0, 0, 0, n, 0};
+    for (int i0 = 0; i0 < n; i0 += 32) {
         const int i = i0 + lane;
-        long long u = 0, t = 0;
-        if (i < p.n_groups) {
-            t = rows_tiles(p, i);
-            u = t * p.hkv * rows_units(rows_len(p.kv_lens, i, p.max_pages));
-        } else if (i < p.n_groups + p.n_own) {
-            u = (long long)p.hkv * rows_units(rows_len(p.own_lens, i - p.n_groups, p.own_max_pages));
+        RowsList r{0, 1, 0, 0};
+        if (i < n) r = rows_list(p, i);
+        const long long ui = warp_scan(r.units, lane);
+        const int ti = (int)warp_scan(i < p.n_groups ? r.tiles : 0, lane);
+        if (n <= 32) U = __shfl_sync(0xffffffffu, ui, 31);
+        if (i0 == 0) {
+            const long long q = rows_share(U, p.num_ctas);
+            c.u0 = min(cta * q, U);
+            c.u1 = min((cta + 1) * q, U);
+            if (c.u0 >= c.u1) return c;
         }
-        const long long ui = warp_scan(u, lane), ti = warp_scan(t, lane);
-        const bool hit = u > 0 && base + ui - u <= r.u0 && r.u0 < base + ui;
+        const bool hit = r.units > 0 && base + ui - r.units <= c.u0 && c.u0 < base + ui;
         const unsigned m = __ballot_sync(0xffffffffu, hit);
         if (m) {
+            int k = 0;   // the (tile, kv head) that holds u0
+            if (hit) {
+                const long long local = c.u0 - (base + ui - r.units), full = (long long)(r.tiles - 1) * p.hkv * r.per * 2;
+                k = local < full ? (int)rows_div(local, 2LL * r.per) : (r.tiles - 1) * p.hkv + (int)rows_div(local - full, (long long)r.last * r.per);
+            }
             const int src = __ffs(m) - 1;
-            r.list = i0 + src;
-            r.first_unit = base + __shfl_sync(0xffffffffu, ui - u, src);
-            r.first_tile = tbase + __shfl_sync(0xffffffffu, ti - t, src);
+            c.list = i0 + src;
+            c.first = base + __shfl_sync(0xffffffffu, ui - r.units, src);
+            c.tile0 = tbase + __shfl_sync(0xffffffffu, ti - (i < p.n_groups ? r.tiles : 0), src);
+            c.k = __shfl_sync(0xffffffffu, k, src);
             break;
         }
         base += __shfl_sync(0xffffffffu, ui, 31);
         tbase += __shfl_sync(0xffffffffu, ti, 31);
     }
-    return r;
+    return c;
 }
 
-// One item's stretch of units inside the CTA.
 struct RowsSeg {
     int own, list;          // own list, or group
-    int j;                  // kv head
+    int j, both;            // kv head; both warpgroups take every unit (tile of more than 128 row heads)
     int row0, rbase, nr;    // first query row of the list, first row head of the tile, row heads in it
-    int len, v0, v1;        // tokens of the list, units [v0, v1) of it
+    int len, per, v0, v1;   // tokens and units of the list, units [v0, v1) of this segment
     long long item;         // record slot: CTA + item
 };
 
-// Walks the segments of a CTA in order.
-struct RowsCursor {
-    long long u, u1, first_unit, first_tile;
-    int list;
-};
-__device__ __forceinline__ RowsCursor rows_cursor(const RowsPlan &r) {
-    return RowsCursor{r.u0, r.u1, r.first_unit, r.first_tile, r.list};
-}
-__device__ __forceinline__ bool rows_next(const RowsParams &p, RowsCursor &c, RowsSeg &s) {
-    while (c.u < c.u1 && c.list < p.n_groups + p.n_own) {
-        const bool own = c.list >= p.n_groups;
-        const int i = own ? c.list - p.n_groups : c.list;
-        const int nt = own ? 1 : rows_tiles(p, i);
-        const int len = own ? rows_len(p.own_lens, i, p.own_max_pages) : rows_len(p.kv_lens, i, p.max_pages);
-        const int per = rows_units(len);
-        const long long total = (long long)nt * p.hkv * per;
-        if (c.u >= c.first_unit + total) {
-            c.first_unit += total;
-            c.first_tile += own ? 0 : nt;
+__device__ __forceinline__ long long ceil_half(long long x, int w) { return w == 2 ? (x + 1) >> 1 : x; }
+
+__device__ __noinline__ bool rows_next(const RowsParams &p, RowsCursor &c, RowsSeg &s) {
+    while (c.list < p.n_groups + p.n_own) {
+        const RowsList r = rows_list(p, c.list);
+        if (r.units == 0 || c.k >= r.tiles * p.hkv) {
+            c.first += r.units;
+            c.tile0 += c.list < p.n_groups ? r.tiles : 0;
             ++c.list;
+            c.k = 0;
             continue;
         }
-        const long long local = c.u - c.first_unit;
-        const int k = (int)(local / per);            // (tile, kv head) of the list
-        const int mt = k / p.hkv;
+        const int mt = c.k / p.hkv, w = mt < r.tiles - 1 ? 2 : r.last;
+        const long long start = c.first + (long long)mt * p.hkv * r.per * 2 + (long long)(c.k - mt * p.hkv) * r.per * w;
+        if (start >= c.u1) return false;
+        s.v0 = (int)ceil_half(max(c.u0 - start, 0LL), w);
+        s.v1 = (int)ceil_half(min(c.u1 - start, (long long)r.per * w), w);
+        const bool own = c.list >= p.n_groups;
+        const int i = own ? c.list - p.n_groups : c.list;
         s.own = own;
         s.list = i;
-        s.j = k - mt * p.hkv;
+        s.j = c.k - mt * p.hkv;
+        s.both = w == 2;
         s.row0 = own ? i : rows_first(p, i);
         s.rbase = mt * kRowsTile;
         s.nr = own ? p.G : min(kRowsTile, (rows_first(p, i + 1) - s.row0) * p.G - s.rbase);
-        s.len = len;
-        s.v0 = (int)(local - (long long)k * per);
-        s.v1 = (int)min((long long)per, s.v0 + (c.u1 - c.u));
-        s.item = own ? (long long)i * p.hkv + s.j : (c.first_tile + mt) * p.hkv + s.j;
-        c.u += s.v1 - s.v0;
-        return true;
+        s.len = own ? rows_len(p.own_lens, i, p.own_max_pages) : rows_len(p.kv_lens, i, p.max_pages);
+        s.per = r.per;
+        s.item = own ? (long long)i * p.hkv + s.j : c.tile0 * p.hkv + c.k;
+        ++c.k;
+        if (s.v0 < s.v1) return true;
     }
     return false;
 }
 
-// Records: a group item's slot holds kRowsTile rows, row (warp w, i) at 16 w + i
-// (warp w = share * wm + row block); an own item's slot 8 shares of G rows.
-__device__ __forceinline__ size_t rows_rec(long long slot, int share, int wm, int row) {
-    return ((size_t)slot * kRowsWarps + (size_t)share * wm + (row >> 4)) * 16 + (row & 15);
+// Record slots of the groups' items.  With own lists every segment is joined with another:
+// slot CTA + item (a CTA's segments are of consecutive items).  Without, only items that cross
+// a CTA's border are: slot 2 CTA for the part of an item that began in an earlier CTA, 2 CTA + 1
+// for one that begins here.
+__device__ __forceinline__ long long rows_slot(const RowsParams &p, long long cta, long long item, bool begins) {
+    return p.n_own ? cta + item : 2 * cta + (begins ? 1 : 0);
 }
-__device__ __forceinline__ size_t rows_own_rec(long long slot, int share, int G, int row) {
-    return ((size_t)slot * kRowsWarps + share) * G + row;
+// Record row: warpgroup g's row r of a slot.
+__device__ __forceinline__ size_t rows_rec(long long slot, int g, int r) { return ((size_t)slot * 2 + g) * kRowsHalf + r; }
+__device__ __forceinline__ size_t rows_own_rec(long long slot, int g, int G, int r) {
+    return ((size_t)slot * 2 + g) * G + r;
 }
-// Blocks of 16 rows a tile of nr row heads is worked on in, rounded up to a power of two.
-__device__ __forceinline__ int rows_blocks(int nr) { return nr <= 16 ? 1 : nr <= 32 ? 2 : nr <= 64 ? 4 : 8; }
 
 // ---------------------------------------------------------------------------
-// operand fetch: what differs between the two caches
+// tcgen05, TMEM and tensor copies
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tm_alloc(uint32_t *dst, int cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tm_dealloc(uint32_t base, int cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Arrive on `bar` when every matrix instruction issued before has completed.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle: groups of 8 rows of 128
+// bytes are `group` bytes apart (high half); `lbo` is the distance of the 64-element
+// blocks along N of an operand whose contiguous dimension is N (low half, with the
+// address: a k-step further is one 32-bit addition).
+__host__ __device__ constexpr uint32_t desc_high(uint32_t group) { return (group >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
+}
+// d (TMEM, 128 x N fp32) (+)= A B with A in shared memory, or in TMEM
+template <uint32_t kGroupA, uint32_t kGroupB>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+                 "r"(desc_high(kGroupA)), "r"(desc_high(kGroupB))
+                 : "memory");
+}
+template <uint32_t kGroupB>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "mov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+                 "r"(desc_high(kGroupB))
+                 : "memory");
+}
+
+// Instruction descriptor: fp32 accumulator, fp16 or BF16 operands, M = 128, N;
+// b_n: B's contiguous dimension is N (else K).
+__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int n, bool b_n) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_n ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// 16 columns of the warp's 32 TMEM lanes: thread = lane, register = column.  The load is
+// asynchronous; tm_ready16 waits for it and carries the registers, so that no use moves ahead.
+#define DQK_R16(X) \
+    X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13), X(14), X(15)
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+#define DQK_OUT(i) "=r"(r[i])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : DQK_R16(DQK_OUT)
+                 : "r"(addr));
+#undef DQK_OUT
+}
+__device__ __forceinline__ void tm_ready16(uint32_t (&r)[16]) {
+#define DQK_INOUT(i) "+r"(r[i])
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : DQK_R16(DQK_INOUT)::"memory");
+#undef DQK_INOUT
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *r) {
+#define DQK_IN(i) "r"(r[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::DQK_R16(
+                     DQK_IN),
+                 "r"(addr)
+                 : "memory");
+#undef DQK_IN
+}
+
+// One box of the pool's tensor map: the 16 token rows from `row` of block `blk`, all columns.
+__device__ __forceinline__ void tensor_copy(void *dst, const CUtensorMap *map, int row, int blk, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+                 "[%6];" ::"r"(smem_addr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(blk), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// INT2 blocks as fp16 operands
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -228,33 +371,16 @@ __device__ __forceinline__ uint16_t bf16_to_f16_sat(uint32_t b) {
     return __half_as_ushort(__float2half_rn(x > 65504.0f ? 65504.0f : x < -65504.0f ? -65504.0f : x));
 }
 
-// The score operand of one page: B registers of k-step s, token halves 0 and 1.
-// BF16: k-step s = channels 16s..16s+15 in order.  INT2: a lane holds channels
-// 32g + 16hi + 4tig + {0..3} of its tokens, taken as the k columns 2tig, 2tig+1,
-// 2tig+8, 2tig+9 of step 2g + hi; the query operand uses the same order.
-template <int D>
-struct PageB16 {
-    static constexpr int kSteps = D / 16;
-    uint32_t blk;
-    int lane;
-    __device__ __forceinline__ void load(uint32_t b, int ln) {
-        blk = b;
-        lane = ln;
-    }
-    __device__ __forceinline__ void keys(int s, uint32_t (&r)[4]) const {   // {b0, b1} tokens 0-7, {b0, b1} tokens 8-15
-        const int mi = lane >> 3, t = (lane & 7) + 8 * (mi >> 1);
-        ldmatrix_x4(r, blk + t * 2 * D + (((2 * s + (mi & 1)) ^ (t & 7)) << 4));
-    }
-    // value operand of channels 16m..16m+15: {b0, b1} of the first 8, {b0, b1} of the next 8
-    __device__ __forceinline__ void values(int m, uint32_t (&r)[4]) const {
-        const int mi = lane >> 3, t = (lane & 7) + 8 * (mi & 1);
-        ldmatrix_x4_trans(r, blk + kPage * 2 * D + t * 2 * D + (((2 * m + (mi >> 1)) ^ (t & 7)) << 4));
-    }
-};
-
+// One packed block in a warp's registers, in the operand order of the stored
+// codes.  keys(s): key channels 16s..16s+15 of the page's 16 tokens, as four
+// 8 x 8 matrices {b0, b1 of tokens 0-7, b0, b1 of tokens 8-15}; a lane holds
+// channels 16s + 4tig + {0, 1} (b0) and + {2, 3} (b1) of token gid, so a row's
+// channels come in the order rows_channel_pos gives, and the query rows use it too.
+// values(m): value channels 16m..16m+15 (rows) by tokens, as matrices
+// {channels 0-7: tokens 0-7, 8-15; channels 8-15: tokens 0-7, 8-15}.
 template <int D, int NS, bool VCH0>
 struct PageInt2 {
-    static constexpr int kSteps = D / 16, NG = D / 32;
+    static constexpr int NG = D / 32;
     uint32_t kw[NG], ks[2][NS], km[2][NS], k0[2];   // k0: fp16 bits of channel 0, token halves
     uint32_t vw[NG], vh[NG], vs[2][NS], vm[2][NS], v0[2];
     int gid, tig;
@@ -359,444 +485,959 @@ struct PageInt2 {
     }
 };
 
+
+// Place of channel c in a key row of the operand tile (and in a prepared query row).
+__host__ __device__ __forceinline__ int rows_channel_pos(int c) {
+    return (c & ~15) + 8 * ((c >> 1) & 1) + 2 * ((c & 15) >> 2) + (c & 1);
+}
+
 // ---------------------------------------------------------------------------
-// the row kernel on warp-wide matrix instructions (m16n8k16): a warp owns 16
-// row heads; the tile's blocks of 16 rows take wm warps, and the 8 / wm warps
-// of a block share the pages of a unit.  kFmt 0: BF16 cache, queries in BF16;
-// 1: BF16 cache, fp32 queries as BF16 high + low parts; 2: INT2 cache.
+// shared memory: operand tiles (K or V of a unit, 128 x D 16-bit values in
+// 128-byte-swizzled rows of 64 columns), query tiles of the two warpgroups (and
+// their low parts, fp32 queries), packed blocks (INT2), barriers.
+//
+// BF16 tile: page after page as one tensor copy lays it, [column block][16 token
+// rows]; the 8-row groups of a half are then a page's size apart.  INT2 tile, keys:
+// [column block][half][page][8 token rows]; values: [half][D channel rows], tokens
+// along the row.
 // ---------------------------------------------------------------------------
+constexpr int kRowsMaxTiles = 8, kRowsMaxRaw = 8;
+struct RowsBars {
+    uint64_t full[kRowsMaxTiles], empty[kRowsMaxTiles];        // operand tiles: the ring of keys, then that of values
+    uint64_t raw_full[kRowsMaxRaw], raw_empty[kRowsMaxRaw];    // packed blocks
+    uint64_t q_full[2], o_step[2], o_full[2], done[2];         // per warpgroup: queries in; a half's product is in the
+                                                               // accumulator, the segment's last one; nothing is in flight
+    uint64_t s_full[2][2], p_full[2][2];                       // per warpgroup and half
+    uint64_t join, read;                                       // the second warpgroup's record is written, has been read
+    uint64_t v_full[kRowsFlags];                               // BF16, by unit: value tile in, stale rows zeroed
+    uint32_t flags[kRowsFlags];                                // pages present, per unit
+    uint32_t tmem;
+    int abort;
+    RowsCursor cursor;
+};
+__host__ __device__ constexpr size_t rows_tile_bytes(int D) { return (size_t)kRowsKv * D * 2; }
+
 template <int D, int kFmt>
-struct RowsState {
-    static constexpr int kSteps = D / 16, kParts = kFmt == 1 ? 2 : 1;
-    uint32_t qa[kParts][kSteps][4];
-    float o[D / 8][4];
-    float m0, m1, l0, l1;    // rows gid, gid + 8 (scores in log2 units)
-    float qs0, qs1;
+struct RowsShape {
+    static constexpr bool kInt2 = kFmt == 2;
+    static constexpr int kParts = kFmt == 1 ? 2 : 1;                   // query parts
+    static constexpr int kThreads = kInt2 ? 512 : 384;
+    static constexpr int kTile = kRowsKv * D * 2;
+    static constexpr int kPageBytes = kPage * D * 2;                   // of a tile
+    // 8-row groups of the keys' half, of the values' (rows of tokens: a page apart; of channels: 1024)
+    static constexpr uint32_t kGroupKv = kInt2 ? 1024 : kPageBytes;
+    static constexpr uint32_t kS0 = 0, kO0 = 256;                      // TMEM columns: S of warpgroup w at 128 w, O at 256 + D w
+    static constexpr uint32_t kIdescS = mma_idesc(!kInt2, kRowsKv / 2, false);
+    static constexpr uint32_t kIdescO = mma_idesc(!kInt2, D, !kInt2);  // BF16 values: channels contiguous
+    static constexpr int kFullCount = kInt2 ? kRowsUnpackWarps : 1;
+    static constexpr float kLift = kInt2 ? kRowsLift : 0.0f;
 };
 
-template <bool F16>
-__device__ __forceinline__ void rows_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16) mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
-    else mma_bf16(d, a[0], a[1], a[2], a[3], b0, b1);
-}
-
-// One page: the first nv of its 16 tokens are the list's (the rest is stale memory).
-template <int D, int kFmt, typename Page>
-__device__ __forceinline__ void rows_page(Page &pg, uint32_t blk, int nv, RowsState<D, kFmt> &st, int lane) {
-    constexpr bool F16 = kFmt == 2;
-    const int tig = lane & 3;
-    pg.load(blk, lane);
-    float c[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[h][e] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-        uint32_t kb[4];
-        pg.keys(s, kb);
-#pragma unroll
-        for (int part = 0; part < RowsState<D, kFmt>::kParts; ++part) {
-            rows_mma<F16>(c[0], st.qa[part][s], kb[0], kb[1]);
-            rows_mma<F16>(c[1], st.qa[part][s], kb[2], kb[3]);
-        }
-    }
-    float s0[4], s1[4];   // rows gid and gid + 8: tokens 2tig, 2tig+1, 2tig+8, 2tig+9
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const bool in = 8 * h + 2 * tig + e < nv;
-            s0[2 * h + e] = in ? c[h][e] * st.qs0 : -INFINITY;
-            s1[2 * h + e] = in ? c[h][2 + e] * st.qs1 : -INFINITY;
-        }
-    float x0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3]));
-    float x1 = fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]));
-    if (__any_sync(0xffffffffu, x0 > st.m0 || x1 > st.m1)) {
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
-        }
-        const float n0 = fmaxf(st.m0, x0), n1 = fmaxf(st.m1, x1);
-        // a row with no finite score yet keeps m = -inf and scales by 1
-        const float a0 = n0 == -INFINITY ? 1.0f : fast_exp2(st.m0 - n0), a1 = n1 == -INFINITY ? 1.0f : fast_exp2(st.m1 - n1);
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-            st.o[n][0] *= a0;
-            st.o[n][1] *= a0;
-            st.o[n][2] *= a1;
-            st.o[n][3] *= a1;
-        }
-        st.l0 *= a0;
-        st.l1 *= a1;
-        st.m0 = n0;
-        st.m1 = n1;
-    }
-    const float b0 = st.m0 == -INFINITY ? 0.0f : st.m0, b1 = st.m1 == -INFINITY ? 0.0f : st.m1;
-    float p0[4], p1[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        p0[e] = fast_exp2(s0[e] - b0);
-        p1[e] = fast_exp2(s1[e] - b1);
-        st.l0 += p0[e];
-        st.l1 += p1[e];
-    }
-    // P~ as the A operand: weights up to 1.  fp16 (INT2) carries them times 2^14, so
-    // that a weight keeps full precision down to 2^-28 (the accumulator is scaled back
-    // in the record).
-    uint32_t pa[4];
-    if constexpr (F16) {
-        pa[0] = pack_f16x2(p0[0] * kRowsPScale, p0[1] * kRowsPScale);
-        pa[1] = pack_f16x2(p1[0] * kRowsPScale, p1[1] * kRowsPScale);
-        pa[2] = pack_f16x2(p0[2] * kRowsPScale, p0[3] * kRowsPScale);
-        pa[3] = pack_f16x2(p1[2] * kRowsPScale, p1[3] * kRowsPScale);
-    } else {
-        pa[0] = pack_bf16x2(p0[0], p0[1]);
-        pa[1] = pack_bf16x2(p1[0], p1[1]);
-        pa[2] = pack_bf16x2(p0[2], p0[3]);
-        pa[3] = pack_bf16x2(p1[2], p1[3]);
-    }
-    const uint32_t vlo = (2 * tig < nv ? 0x0000ffffu : 0u) | (2 * tig + 1 < nv ? 0xffff0000u : 0u);
-    const uint32_t vhi = (2 * tig + 8 < nv ? 0x0000ffffu : 0u) | (2 * tig + 9 < nv ? 0xffff0000u : 0u);
-#pragma unroll
-    for (int m = 0; m < D / 16; ++m) {
-        uint32_t vb[4];
-        pg.values(m, vb);
-        rows_mma<F16>(st.o[2 * m], pa, vb[0] & vlo, vb[1] & vhi);
-        rows_mma<F16>(st.o[2 * m + 1], pa, vb[2] & vlo, vb[3] & vhi);
-    }
-}
-
-// The query operand of rows r, r + 8 of the tile (row heads rb + 0..15).
-template <int D, int kFmt>
-__device__ __forceinline__ void rows_queries(const RowsParams &p, const RowsSeg &s, int rb, RowsState<D, kFmt> &st,
-                                             int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
-    size_t at[2];
-    bool in[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = rb + gid + 8 * h;
-        in[h] = r < s.nr;
-        const int rr = s.rbase + (in[h] ? r : 0), row = s.row0 + rr / p.G, hh = rr % p.G;
-        at[h] = (size_t)row * p.hq + (size_t)s.j * p.G + hh;
-    }
-    if constexpr (kFmt == 2) {
-        st.qs0 = in[0] ? p.q_scale[at[0]] : 0.0f;
-        st.qs1 = in[1] ? p.q_scale[at[1]] : 0.0f;
-    } else {
-        st.qs0 = st.qs1 = p.qs;
-    }
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t lo = 0u, hi = 0u, lo2 = 0u, hi2 = 0u;   // k columns 2tig, 2tig+1 and 2tig+8, 2tig+9
-            if (in[h]) {
-                if constexpr (kFmt == 2) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p.q) + at[h] * D +
-                                                                     16 * k + 4 * tig);
-                    lo = w.x;
-                    hi = w.y;
-                } else if constexpr (kFmt == 0) {
-                    const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + at[h] * D + 16 * k + 2 * tig;
-                    lo = *reinterpret_cast<const uint32_t *>(q);
-                    hi = *reinterpret_cast<const uint32_t *>(q + 8);
-                } else {
-                    const float *q = reinterpret_cast<const float *>(p.q) + at[h] * D + 16 * k + 2 * tig;
-                    const float2 a = *reinterpret_cast<const float2 *>(q), b = *reinterpret_cast<const float2 *>(q + 8);
-                    lo = pack_bf16x2(a.x, a.y);
-                    hi = pack_bf16x2(b.x, b.y);
-                    lo2 = pack_bf16x2(a.x - __uint_as_float(lo << 16), a.y - __uint_as_float(lo & 0xffff0000u));
-                    hi2 = pack_bf16x2(b.x - __uint_as_float(hi << 16), b.y - __uint_as_float(hi & 0xffff0000u));
-                }
-            }
-            st.qa[0][k][h] = lo;
-            st.qa[0][k][2 + h] = hi;
-            if constexpr (kFmt == 1) {
-                st.qa[1][k][h] = lo2;
-                st.qa[1][k][2 + h] = hi2;
-            }
-        }
-    st.m0 = st.m1 = -INFINITY;
-    st.l0 = st.l1 = 0.0f;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.0f;
-}
-
-template <int D, int kFmt>
-__device__ __forceinline__ void rows_record(const RowsParams &p, const RowsSeg &s, int cta, int share, int wm, int rb,
-                                            RowsState<D, kFmt> &st, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
-        st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
-    }
-    constexpr float kBack = kFmt == 2 ? 1.0f / kRowsPScale : 1.0f;
-    if (!s.own && cta + s.item >= p.rec_slots) {   // groups that overlap
-        if (lane == 0) dqk_flag_error(kErrBounds);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = rb + gid + 8 * h;
-        if (r >= s.nr) continue;
-        float *rec = (s.own ? p.own_rec + rows_own_rec(cta + s.item, share, p.G, r) * rec_stride(D)
-                            : p.rec + rows_rec(cta + s.item, share, wm, r) * rec_stride(D));
-        if (tig == 0) {
-            rec[0] = h ? st.m1 : st.m0;
-            rec[1] = h ? st.l1 : st.l0;
-        }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2 *>(rec + kRecHead + 8 * n + 2 * tig) =
-                make_float2(st.o[n][2 * h] * kBack, st.o[n][2 * h + 1] * kBack);
-    }
-}
-
-// Brings the CTA's units into the ring, one stage each: lane l < 8 copies page l
-// of the unit (one block of the item's kv head).  Pages past the list's end and
-// bad page ids are marked absent.
-__device__ __forceinline__ void rows_producer(const RowsParams &p, const RowsPlan &plan, unsigned char *stage_mem,
-                                              uint64_t *full, uint64_t *empty, unsigned char *valid,
-                                              volatile int *abort_flag, int lane) {
-    const int S = p.stages;
-    const uint32_t stage_bytes = (uint32_t)(kRowsPages * p.bb);
-    RowsCursor cur = rows_cursor(plan);
-    RowsSeg s;
-    int stage = 0, filled = 0;
+// A place in a ring of n stages and the parity of its round.
+struct RowsRing {
+    int st = 0;
     uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++st == n) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The units of a CTA in order, for the matrix threads.
+struct RowsUnits {
+    RowsCursor cur;
+    RowsSeg s;
+    RowsRing k, t;     // places of the unit's key tile and of its value tile
+    int v, n, unit;    // unit of the item, jobs and units before it
+    bool live;
+    __device__ __forceinline__ void start(const RowsParams &p, const RowsCursor &c) {
+        cur = c;
+        n = unit = 0;
+        live = rows_next(p, cur, s);
+        v = live ? s.v0 : 0;
+    }
+    __device__ __forceinline__ bool mine(int w) const { return s.both || ((n ^ w) & 1) == 0; }
+    __device__ __forceinline__ bool first() const { return s.both ? v == s.v0 : v < s.v0 + 2; }   // of a warpgroup's in the segment
+    __device__ __forceinline__ bool last() const { return s.both ? v == s.v1 - 1 : v >= s.v1 - 2; }
+    __device__ __forceinline__ void next(const RowsParams &p) {
+        n += s.both ? 2 : 1;
+        ++unit;
+        k.next(p.ktiles);
+        t.next(p.vtiles);
+        if (++v == s.v1) {
+            live = rows_next(p, cur, s);
+            v = live ? s.v0 : 0;
+        }
+    }
+};
+
+// A bounded wait that, when it runs out, reports and raises the abort flag, on which every role ends.
+__device__ __noinline__ bool rows_wait_long(uint64_t *bar, uint32_t phase, RowsBars &B, unsigned long long ns) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, phase)) return true;
+        if ((it & 63u) == 0u) {
+            if (*(volatile int *)&B.abort) return false;
+            if (global_timer_ns() - t0 > ns) {
+                *(volatile int *)&B.abort = 1;
+                dqk_flag_error(kErrTimeout);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool rows_wait(uint64_t *bar, uint32_t phase, RowsBars &B, unsigned long long ns) {
+    for (int i = 0; i < 16; ++i)
+        if (mbar_try_wait(bar, phase)) return true;
+    return rows_wait_long(bar, phase, B, ns);
+}
+
+template <int D, int kFmt>
+__device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtensorMap *map, RowsBars &B, unsigned char *tiles,
+                                              unsigned char *raw, int lane) {
+    using T = RowsShape<D, kFmt>;
+    RowsCursor cur = B.cursor;
+    RowsSeg s;
+    RowsRing ring[2];   // raw blocks, or key and value tiles
+    int unit = 0;
     bool ok = true;
+    const int pg = lane & (kRowsPages - 1), h = lane >> 3;   // lanes 0 .. 7 copy a page each
     while (ok && rows_next(p, cur, s)) {
         const int *tab = s.own ? p.own_table + (size_t)s.list * p.own_max_pages : p.table + (size_t)s.list * p.max_pages;
         const int npages = (s.len + kPage - 1) / kPage;
         if (lane == 0 && (s.own ? p.own_lens[s.list] : p.kv_lens[s.list]) > s.len) dqk_flag_error(kErrBounds);
-        for (int v = s.v0; v < s.v1; ++v) {
-            const int page = v * kRowsPages + lane;
-            const bool in = lane < kRowsPages && page < npages;
-            const int phys = in ? tab[page] : -1;
+        int page = s.v0 * kRowsPages + pg;
+        int phys = page < npages ? tab[page] : -1;
+        for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
+            const bool in = page < npages;
             const bool have = in && phys >= 0 && phys < p.num_pages;
-            if (in && !have) dqk_flag_error(kErrBounds);
-            int good = 1;
-            if (lane == 0) good = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.wait_ns, 2000u) && !*abort_flag;
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
+            const int blk = have ? phys * p.hkv + s.j : 0;
+            if (in && !have && h == 0) dqk_flag_error(kErrBounds);
+            page += kRowsPages;
+            phys = page < npages ? tab[page] : -1;   // the next unit's, on its way while this one waits
+            const uint32_t m = __ballot_sync(0xffffffffu, have) & ((1u << kRowsPages) - 1u);
+            const int nb = __popc(m);
+            if constexpr (T::kInt2) {
+                ok = __all_sync(0xffffffffu, rows_wait(&B.raw_empty[ring[0].st], ring[0].phase ^ 1u, B, p.wait_ns));
+                if (!ok) break;
                 if (lane == 0) {
-                    *abort_flag = 1;
-                    dqk_flag_error(kErrTimeout);
+                    B.flags[unit & (kRowsFlags - 1)] = m;
+                    mbar_arrive_expect_tx(&B.raw_full[ring[0].st], nb * (uint32_t)p.bb);
                 }
-                ok = false;
-                break;
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, have);
-            if (lane < kRowsPages) valid[stage * kRowsPages + lane] = have;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(m) * (uint32_t)p.bb);
-            __syncwarp();
-            if (have)
-                bulk_copy_g2s(stage_mem + (size_t)stage * stage_bytes + (size_t)lane * p.bb,
-                              p.pool + ((size_t)phys * p.hkv + s.j) * p.bb, (uint32_t)p.bb, &full[stage]);
-            ++filled;
-            if (++stage == S) {
-                stage = 0;
-                phase ^= 1u;
+                __syncwarp();
+                if (h == 0 && have)
+                    bulk_copy_g2s(raw + ((size_t)ring[0].st * kRowsPages + pg) * p.bb, p.pool + (size_t)blk * p.bb, (uint32_t)p.bb,
+                                  &B.raw_full[ring[0].st]);
+                ring[0].next(p.raw_stages);
+            } else {
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int st = ring[kv].st + (kv ? p.ktiles : 0);
+                    ok = ok && __all_sync(0xffffffffu, rows_wait(&B.empty[st], ring[kv].phase ^ 1u, B, p.wait_ns));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (kv == 0) B.flags[unit & (kRowsFlags - 1)] = m;
+                        mbar_arrive_expect_tx(&B.full[st], nb * (uint32_t)T::kPageBytes);
+                    }
+                    __syncwarp();
+                    if (h == 0 && have)
+                        tensor_copy(tiles + (size_t)st * T::kTile + pg * T::kPageBytes, map, kv * kPage, blk, &B.full[st]);
+                    ring[kv].next(kv ? p.vtiles : p.ktiles);
+                }
             }
         }
     }
-    // never leave with copies in flight
-    if (lane == 0)
-        for (int k = filled - 1; k >= 0 && k >= filled - S; --k)
-            (void)mbar_wait_bounded(&full[k % S], (uint32_t)(k / S) & 1u, p.wait_ns);
+    // never leave with copies in flight, nor before the last arrivals on `empty`: every stage that was filled has
+    // landed and (unless aborted) been released -- a stage's last round is the one before the ring's place, or the
+    // present one if the place has passed it
+    for (int kv = 0; kv < (T::kInt2 ? 1 : 2); ++kv) {
+        const int n = T::kInt2 ? p.raw_stages : kv ? p.vtiles : p.ktiles, first = kv ? p.ktiles : 0;
+        uint64_t *full = T::kInt2 ? B.raw_full : B.full, *empty = T::kInt2 ? B.raw_empty : B.empty;
+        for (int st = 0; st < n; ++st) {
+            if (st >= ring[kv].st && unit < n) continue;   // never filled
+            const uint32_t phase = ring[kv].phase ^ (st >= ring[kv].st ? 1u : 0u);
+            (void)mbar_wait_bounded(&full[first + st], phase, p.wait_ns);
+            (void)rows_wait(&empty[first + st], phase, B, p.wait_ns);
+        }
+    }
 }
 
-// Shared memory besides the ring: full, empty, valid flags, abort flag.
-constexpr size_t kRowsFixedSmem = 2 * kMaxStages * 8 + kMaxStages * kRowsPages + 16;
-
-template <int D, int kFmt, int NS, bool VCH0>
-__global__ void __launch_bounds__(kRowsThreads, 1) k_rows(const __grid_constant__ RowsParams p) {
-    extern __shared__ __align__(128) unsigned char rows_smem[];
-    const int S = p.stages;
-    const uint32_t stage_bytes = (uint32_t)(kRowsPages * p.bb);
-    unsigned char *stage_mem = rows_smem;
-    uint64_t *full = reinterpret_cast<uint64_t *>(rows_smem + (size_t)S * stage_bytes);
-    uint64_t *empty = full + kMaxStages;
-    unsigned char *valid = reinterpret_cast<unsigned char *>(empty + kMaxStages);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(valid + kMaxStages * kRowsPages);
-    __shared__ RowsPlan sh_plan;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dependency_wait();
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kRowsWarps);
-        }
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 0) {
-        const RowsPlan r = rows_plan(p, blockIdx.x, p.num_ctas, lane);
-        if (lane == 0) sh_plan = r;
-    }
-    __syncthreads();
-    const RowsPlan plan = sh_plan;
-    if (warp == kRowsWarps) {
-        rows_producer(p, plan, stage_mem, full, empty, valid, abort_flag, lane);
-        return;
-    }
-    RowsCursor cur = rows_cursor(plan);
+// INT2: packed blocks -> fp16 operand tiles.  Keys as rows of tokens; values as
+// rows of channels (the order their codes are stored in), 64 tokens per 128-byte row.
+template <int D, int NS, bool VCH0>
+__device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *raw, int warp,
+                                            int lane) {
+    constexpr int kTile = kRowsKv * D * 2;
+    RowsCursor cur = B.cursor;
     RowsSeg s;
-    RowsState<D, kFmt> st;
-    int stage = 0;
-    uint32_t phase = 0;
+    RowsRing rr, rk, rv;
+    int unit = 0;
+    bool ok = true;
+    const int mi = lane >> 3, r8 = lane & 7, tig = lane & 3;
+    while (ok && rows_next(p, cur, s)) {
+        for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
+            const int rs = rr.st;
+            ok = rows_wait(&B.raw_full[rs], rr.phase, B, p.wait_ns);
+            rr.next(p.raw_stages);
+            const int sk = rk.st, sv = p.ktiles + rv.st;
+            ok = ok && rows_wait(&B.empty[sk], rk.phase ^ 1u, B, p.wait_ns);
+            ok = ok && rows_wait(&B.empty[sv], rv.phase ^ 1u, B, p.wait_ns);
+            rk.next(p.ktiles);
+            rv.next(p.vtiles);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
+            const uint32_t kt = smem_addr(tiles) + (uint32_t)sk * kTile, vt = smem_addr(tiles) + (uint32_t)sv * kTile;
+#pragma unroll 1
+            for (int pg = warp; pg < kRowsPages; pg += kRowsUnpackWarps) {
+                // rows of the matrix this lane addresses: keys, token 8 (mi >> 1) + r8 of the page, column chunk
+                // 2s + (mi & 1); values, channel 16m + 8 (mi >> 1) + r8, the page's tokens of half mi & 1
+                const uint32_t ka = kt + (uint32_t)(64 * (mi >> 1) + 8 * pg + r8) * 128;
+                const uint32_t va = vt + (uint32_t)(mi & 1) * (D * 128) + (uint32_t)(8 * (mi >> 1) + r8) * 128 +
+                                    (uint32_t)((pg ^ r8) << 4);
+                if ((have >> pg) & 1u) {
+                    PageInt2<D, NS, VCH0> b;
+                    b.load(smem_addr(raw) + (uint32_t)((rs * kRowsPages + pg) * p.bb), lane);
+#pragma unroll
+                    for (int st = 0; st < D / 16; ++st) {
+                        uint32_t k4[4];
+                        b.keys(st, k4);
+                        const int c = 2 * st + (mi & 1);
+                        stmatrix_x4(ka + (uint32_t)(c >> 3) * (kRowsKv * 128) + (uint32_t)(((c & 7) ^ r8) << 4), k4);
+                    }
+                    // tokens past the list's end hold stale bytes: zeros, so that they add nothing
+                    const int nv = s.len - (v * kRowsPages + pg) * kPage;
+                    const uint32_t lo = (2 * tig < nv ? 0x0000ffffu : 0u) | (2 * tig + 1 < nv ? 0xffff0000u : 0u);
+                    const uint32_t hi = (2 * tig + 8 < nv ? 0x0000ffffu : 0u) | (2 * tig + 9 < nv ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        uint32_t v4[4];
+                        b.values(m, v4);
+                        v4[0] &= lo;
+                        v4[1] &= hi;
+                        v4[2] &= lo;
+                        v4[3] &= hi;
+                        stmatrix_x4(va + (uint32_t)(m * 16 * 128), v4);
+                    }
+                } else {
+                    const uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) stmatrix_x4(va + (uint32_t)(m * 16 * 128), z);
+                }
+            }
+            fence_proxy_async_shared();   // the tiles are read by the tensor core
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&B.full[sk]);
+                mbar_arrive(&B.full[sv]);
+                mbar_arrive(&B.raw_empty[rs]);
+            }
+        }
+    }
+    // the last arrivals on `empty` come before the block leaves
+    for (int kv = 0; kv < 2; ++kv) {
+        const RowsRing r = kv ? rv : rk;
+        const int n = kv ? p.vtiles : p.ktiles;
+        for (int st = 0; st < n; ++st)
+            if (st < r.st || unit >= n)
+                (void)rows_wait(&B.empty[(kv ? p.ktiles : 0) + st], r.phase ^ (st >= r.st ? 1u : 0u), B, p.wait_ns);
+    }
+}
+
+// BF16: zeros the value rows of tokens that are not the list's (the tensor copies
+// brought stale memory, or nothing, there) before the tile's first use.
+template <int D>
+__device__ __forceinline__ void rows_tails(const RowsParams &p, RowsBars &B, unsigned char *tiles, int lane) {
+    constexpr int kChunks = D / 8, kTile = kRowsKv * D * 2;
+    RowsCursor cur = B.cursor;
+    RowsSeg s;
+    RowsRing ring;
+    int unit = 0;
     bool ok = true;
     while (ok && rows_next(p, cur, s)) {
-        const int wm = rows_blocks(s.nr), share = warp / wm, shares = kRowsWarps / wm, rb = 16 * (warp % wm);
-        rows_queries<D, kFmt>(p, s, rb, st, lane);
-        for (int v = s.v0; v < s.v1; ++v) {
-            if (!mbar_wait_bounded(&full[stage], phase, p.wait_ns)) {
-                if (lane == 0) {
-                    *abort_flag = 1;
-                    dqk_flag_error(kErrTimeout);
+        for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
+            ok = __all_sync(0xffffffffu, rows_wait(&B.full[p.ktiles + ring.st], ring.phase, B, p.wait_ns));
+            if (!ok) break;
+            const int nv = s.len - v * kRowsKv;
+            const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
+            if (nv < kRowsKv || have != (1u << kRowsPages) - 1u) {
+                const uint32_t tile = smem_addr(tiles) + (uint32_t)(p.ktiles + ring.st) * kTile;
+                const int from = have == (1u << kRowsPages) - 1u ? nv : 0;   // all pages there: the rows behind the end
+                for (int i = from * kChunks + lane; i < kRowsKv * kChunks; i += 32) {
+                    const int row = i / kChunks, c = i % kChunks, pg = row >> 4;
+                    if (row >= nv || !((have >> pg) & 1u))
+                        st_s128(tile + (uint32_t)(pg * (kPage * D * 2) + (c >> 3) * (kPage * 128) + (row & 15) * 128 + (c & 7) * 16),
+                                make_uint4(0u, 0u, 0u, 0u));
                 }
-                ok = false;
-                break;
+                fence_proxy_async_shared();
+                __syncwarp();
             }
-            const uint32_t base = smem_addr(stage_mem) + (uint32_t)stage * stage_bytes;
-            if (rb < s.nr) {
-                for (int k = share; k < kRowsPages; k += shares) {
-                    if (!valid[stage * kRowsPages + k]) continue;
-                    const int nv = s.len - (v * kRowsPages + k) * kPage;
-                    if constexpr (kFmt == 2) {
-                        PageInt2<D, NS, VCH0> pg;
-                        rows_page<D, kFmt>(pg, base + (uint32_t)(k * p.bb), nv, st, lane);
+            if (lane == 0) mbar_arrive(&B.v_full[unit & (kRowsFlags - 1)]);
+            ring.next(p.vtiles);
+        }
+    }
+}
+
+// The matrix thread of warpgroup w.  Half h of the next job's scores follows half h of this
+// job's outputs, whose weights lie in the same columns.  Tiles of units that are the other
+// warpgroup's alone are released here too (two arrivals free a tile).
+template <int D, int kFmt>
+__device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *qmem,
+                                            uint32_t tmem, int w) {
+    using T = RowsShape<D, kFmt>;
+    const uint32_t tile0 = smem_addr(tiles), q0 = smem_addr(qmem) + (uint32_t)(w * T::kParts * T::kTile);
+    const uint32_t tS = tmem + T::kS0 + 128 * w, tO = tmem + T::kO0 + D * w;
+    uint32_t qn = 0, pn = 0;    // parities of the next waits on q_full, p_full
+    bool ok = true;
+    RowsUnits nx;               // the next unit that is this warpgroup's
+    nx.start(p, B.cursor);
+    bool key_seen = false;      // of a unit to be passed over: its key tile is released
+    // Moves nx on; false: not there yet (a tile to be passed over has not landed), or abort.
+    auto seek = [&](bool block) {
+        while (nx.live && !nx.mine(w)) {
+            const int kt = nx.k.st, vt = p.ktiles + nx.t.st;
+            if (!key_seen) {
+                if (!(block ? rows_wait(&B.full[kt], nx.k.phase, B, p.wait_ns) : mbar_test_wait(&B.full[kt], nx.k.phase))) return false;
+                mbar_arrive(&B.empty[kt]);
+                key_seen = true;
+            }
+            if (!(block ? rows_wait(&B.full[vt], nx.t.phase, B, p.wait_ns) : mbar_test_wait(&B.full[vt], nx.t.phase))) return false;
+            mbar_arrive(&B.empty[vt]);
+            key_seen = false;
+            nx.next(p);
+        }
+        return true;
+    };
+    auto scores = [&](int h) {
+        const uint32_t b = desc_low(tile0 + (uint32_t)nx.k.st * T::kTile + (uint32_t)h * (T::kInt2 ? kRowsKv / 2 * 128 : 1024), 16);
+#pragma unroll
+        for (int part = 0; part < T::kParts; ++part) {
+            const uint32_t a = desc_low(q0 + (uint32_t)(part * T::kTile), 16);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t qo = (uint32_t)((s >> 2) * (kRowsKv * 128) + (s & 3) * 32) >> 4;
+                const uint32_t ko = (uint32_t)((s >> 2) * (T::kInt2 ? kRowsKv * 128 : kPage * 128) + (s & 3) * 32) >> 4;
+                mma_ss<1024, T::kGroupKv>(tS + 64 * h, a + qo, b + ko, T::kIdescS, s > 0 || part > 0 ? 1u : 0u);
+            }
+        }
+        mma_commit(&B.s_full[w][h]);
+    };
+    // Waits for what the next job's scores read.
+    auto operands = [&]() {
+        if (nx.first()) {
+            if (!rows_wait(&B.q_full[w], qn, B, p.wait_ns)) return false;
+            qn ^= 1u;
+        }
+        return rows_wait(&B.full[nx.k.st], nx.k.phase, B, p.wait_ns);
+    };
+    ok = seek(true);
+    if (ok && nx.live) {
+        ok = operands();
+        if (ok) {
+            tm_fence_after();
+            scores(0);
+            scores(1);
+            mma_commit(&B.empty[nx.k.st]);
+        }
+    }
+    while (ok && nx.live) {
+        // this job (nx moves on to the one after)
+        const int vt = p.ktiles + nx.t.st, unit = nx.unit;
+        const uint32_t vphase = nx.t.phase;
+        const uint32_t acc = nx.first() ? 0u : 1u;
+        const bool last = nx.last();
+        // BF16: rows of tokens, contiguous channels; INT2: rows of channels, contiguous tokens
+        const uint32_t b = desc_low(tile0 + (uint32_t)vt * T::kTile, T::kInt2 ? 16 : kPage * 128);
+        nx.next(p);
+        ok = T::kInt2 ? rows_wait(&B.full[vt], vphase, B, p.wait_ns)
+                      : rows_wait(&B.v_full[unit & (kRowsFlags - 1)], (unit / kRowsFlags) & 1, B, p.wait_ns);
+        bool ahead = false;   // the next job's first half is on its way
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // the next job's operands, if they are there (an item's queries are loaded after the item before is finished)
+            const bool early = h == 0 && ok && seek(false) && nx.live && !nx.first() && mbar_test_wait(&B.full[nx.k.st], nx.k.phase);
+            ok = ok && rows_wait(&B.p_full[w][h], pn, B, p.wait_ns);
+            if (!ok) break;
+            tm_fence_after();
+#pragma unroll
+            for (int s = 0; s < kRowsKv / 32; ++s) {
+                const uint32_t off = (uint32_t)(T::kInt2 ? h * (D * 128) + s * 32 : 2 * s * T::kPageBytes + h * 1024) >> 4;
+                mma_ts<T::kGroupKv>(tO, tS + 64 * h + 8 * s, b + off, T::kIdescO, h > 0 || s > 0 ? 1u : acc);
+            }
+            mma_commit(&B.o_step[w]);
+            if (h == 0) {
+                if (early) scores(0);
+                ahead = early;
+            }
+        }
+        if (!ok) break;
+        pn ^= 1u;
+        if (last) mma_commit(&B.o_full[w]);
+        if (ahead) {
+            scores(1);
+            mma_commit(&B.empty[nx.k.st]);
+        }
+        mma_commit(&B.empty[vt]);
+        if (!ahead) {
+            ok = seek(true);
+            if (ok && nx.live) {
+                ok = operands();
+                if (!ok) break;
+                tm_fence_after();
+                scores(0);
+                scores(1);
+                mma_commit(&B.empty[nx.k.st]);
+            }
+        }
+    }
+    // nothing in flight when the block leaves (after an abort too)
+    mma_commit(&B.done[w]);
+    (void)mbar_wait_bounded(&B.done[w], 0u, p.wait_ns);
+}
+
+// Scores of half h of a unit whose tokens are not all the list's (its last unit, or an absent page): token t
+// is one if t < nv and its page is present; the others' scores become -inf, in place.
+__device__ __forceinline__ void rows_mask(uint32_t tS, int nv, uint32_t have, int h) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {   // 16 columns: half the tokens of pages 2c and 2c + 1
+        uint32_t u[16];
+        tm_ld16(tS + 16 * c, u);
+        tm_ready16(u);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int pg = 2 * c + g, n = (have >> pg) & 1u ? nv - kPage * pg - 8 * h : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= n) u[8 * g + i] = 0xff800000u;
+        }
+        tm_st16(tS + 16 * c, u);
+    }
+    tm_wait_st();
+}
+
+// 16 scores of a thread's row -> weights 2^(x qs - base), packed in pairs; their sum is added to
+// s0, s1 and their largest score taken into m0, m1.
+template <bool F16>
+__device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2, float2 b2, uint32_t *pk, float2 &s0, float2 &s1,
+                                             float &m0, float &m1) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float2 a = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+        const float2 b = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
+        m0 = max3(m0, a.x, a.y);
+        m1 = max3(m1, b.x, b.y);
+        const float2 ea = fma2(a, q2, b2), eb = fma2(b, q2, b2);
+        const float2 pa = make_float2(fast_exp2(ea.x), fast_exp2(ea.y)), pb = make_float2(fast_exp2(eb.x), fast_exp2(eb.y));
+        s0 = add2(s0, pa);
+        s1 = add2(s1, pb);
+        pk[i / 2] = F16 ? pack_f16x2(pa.x, pa.y) : pack_bf16x2(pa.x, pa.y);
+        pk[i / 2 + 1] = F16 ? pack_f16x2(pb.x, pb.y) : pack_bf16x2(pb.x, pb.y);
+    }
+}
+
+// The accumulator's row times f.
+template <int D>
+__device__ __forceinline__ void rows_rescale(uint32_t tO, float f) {
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tm_ld16(tO + 16 * c, o);
+        tm_ready16(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tm_st16(tO + 16 * c, o);
+    }
+}
+
+// The largest score of a first half.
+__device__ __forceinline__ float rows_largest(uint32_t tS, float qs) {
+    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t u[16];
+        tm_ld16(tS + 16 * c, u);
+        tm_ready16(u);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            m0 = max3(m0, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+            m1 = max3(m1, __uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
+        }
+    }
+    return fmaxf(m0, m1) * qs;
+}
+
+// The weights of a thread's row for half a unit: S (64 columns at tS) becomes P~
+// (packed pairs, its first 32 columns), and the reference m and the sum l of the row follow.  A half
+// whose scores pass the reference by more than the slack (rare) is taken again after the reference
+// has moved and what was summed -- l, and the accumulator, once `settled` has waited for it -- has been rescaled.
+template <int D, bool F16, typename Settled>
+__device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, float qs, float lift, float &m, float &l,
+                                          Settled settled) {
+    uint32_t pk[32];
+    const float2 q2 = make_float2(qs, qs);
+    float base = (m == -INFINITY ? 0.0f : m) - lift;
+    float2 b2 = make_float2(-base, -base), s0 = make_float2(0.0f, 0.0f), s1 = s0;
+    float m0 = -INFINITY, m1 = -INFINITY;
+    constexpr int kAtOnce = F16 ? 2 : 4;   // 16-column loads in registers together (INT2: 128 registers a thread)
+#pragma unroll
+    for (int c0 = 0; c0 < 4; c0 += kAtOnce) {
+        uint32_t x[kAtOnce][16];
+#pragma unroll
+        for (int c = 0; c < kAtOnce; ++c) tm_ld16(tS + 16 * (c0 + c), x[c]);
+#pragma unroll
+        for (int c = 0; c < kAtOnce; ++c) tm_ready16(x[c]);
+#pragma unroll
+        for (int c = 0; c < kAtOnce; ++c) rows_weights<F16>(x[c], q2, b2, pk + 8 * (c0 + c), s0, s1, m0, m1);
+    }
+    const float mx = fmaxf(m0, m1) * qs;
+    const bool move = mx > m + kRowsSlack;
+    if (__any_sync(0xffffffffu, move)) {
+        // the references are whole numbers: moving one scales by a power of two
+        const float to = move ? ceilf(mx) : m, f = !move || m == -INFINITY ? 1.0f : fast_exp2(m - to);
+        m = to;
+        l *= f;
+        int acc = settled();   // 1: the accumulator holds earlier halves, 0: nothing yet, -1: abort
+        if (acc < 0) return false;
+        if (acc) rows_rescale<D>(tO, f);
+        base = (m == -INFINITY ? 0.0f : m) - lift;
+        b2 = make_float2(-base, -base);
+        s0 = s1 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t y[16];
+            tm_ld16(tS + 16 * c, y);
+            tm_ready16(y);
+            rows_weights<F16>(y, q2, b2, pk + 8 * c, s0, s1, m0, m1);
+        }
+    }
+    l += (s0.x + s0.y) + (s1.x + s1.y);
+    tm_st16(tS, pk);
+    tm_st16(tS + 16, pk + 16);
+    tm_wait_st();
+    return true;
+}
+
+// Softmax warpgroup w: thread = row head.
+template <int D, int kFmt>
+__device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, unsigned char *qmem, uint32_t tmem, int w, int cta) {
+    using T = RowsShape<D, kFmt>;
+    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t tS = tmem + lanes + T::kS0 + 128 * w, tO = tmem + lanes + T::kO0 + D * w;
+    RowsCursor cur = B.cursor;
+    RowsSeg s;
+    int n = 0, unit0 = 0;                     // jobs and units before the segment
+    uint32_t jobs = 0, pn = 0, on = 0, jn = 0, rn = 0;   // jobs and halves done; waits done on o_full, join, read
+    bool ok = true, pending = false;          // pending (second warpgroup): a record the first has yet to read
+    while (ok && rows_next(p, cur, s)) {
+        const int units = s.v1 - s.v0;
+        const int step = s.both ? 1 : 2;                                  // this warpgroup's units: vf, vf + step, ...
+        const int vf = s.both ? s.v0 : s.v0 + ((n ^ w) & 1);
+        const int rows = s.both ? s.nr - kRowsHalf * w : s.nr;            // its row heads (r < rows)
+        const bool mine = vf < s.v1, valid = r < rows, any = 32 * quad < rows;
+        const int rr = s.rbase + (s.both ? kRowsHalf * w : 0) + r;
+        const size_t at = valid ? (size_t)(s.row0 + rr / p.G) * p.hq + (size_t)s.j * p.G + rr % p.G : 0;
+        float m = -INFINITY, l = 0.0f, qs = p.qs;
+        if (mine) {
+            if (valid) {
+                if constexpr (kFmt == 2) qs = p.q_scale[at];
+                const uint32_t row = smem_addr(qmem) + (uint32_t)(w * T::kParts * T::kTile) + (uint32_t)r * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t dst = row + (uint32_t)((c >> 3) * (kRowsKv * 128) + (((c & 7) ^ (r & 7)) << 4));
+                    if constexpr (kFmt != 1) {
+                        st_s128(dst, *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + at * D + 8 * c));
                     } else {
-                        PageB16<D> pg;
-                        rows_page<D, kFmt>(pg, base + (uint32_t)(k * p.bb), nv, st, lane);
+                        const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + at * D + 8 * c);
+                        const float4 a = f[0], b = f[1];
+                        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                            lo[i] = pack_bf16x2(x[2 * i] - __uint_as_float(hi[i] << 16),
+                                                x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
+                        }
+                        st_s128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        st_s128(dst + T::kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                     }
                 }
             }
+            fence_proxy_async_shared();
             __syncwarp();
-            mbar_arrive_if(&empty[stage], lane == 0);
-            if (++stage == S) {
-                stage = 0;
-                phase ^= 1u;
+            if (lane == 0) mbar_arrive(&B.q_full[w]);
+        }
+        for (int v = vf; ok && v < s.v1; v += step) {
+            const int nv = s.len - v * kRowsKv;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h, ++pn) {
+                ok = __all_sync(0xffffffffu, rows_wait(&B.s_full[w][h], jobs & 1u, B, p.wait_ns));
+                if (!ok) break;
+                tm_fence_after();
+                if (any) {   // warps whose 32 rows are all past the tile leave the weights as they are: rows do not mix
+                    const uint32_t have = B.flags[(unit0 + v - s.v0) & (kRowsFlags - 1)];
+                    if (nv < kRowsKv || have != (1u << kRowsPages) - 1u) rows_mask(tS + 64 * h, nv, have, h);
+                    const bool none = v == vf && h == 0;
+                    if (none) m = ceilf(rows_largest(tS, qs));   // no reference yet
+                    // the half before this one may still be on its way into the accumulator (the one before that is not:
+                    // these scores lie where its weights were)
+                    ok = rows_half<D, kFmt == 2>(tS + 64 * h, tO, qs, T::kLift, m, l, [&]() {
+                        if (none) return 0;
+                        if (!__all_sync(0xffffffffu, rows_wait(&B.o_step[w], (pn - 1) & 1u, B, p.wait_ns))) return -1;
+                        tm_fence_after();
+                        return 1;
+                    });
+                    if (!ok) break;
+                }
+                tm_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.p_full[w][h]);
+            }
+            ++jobs;
+        }
+        if (!ok) break;
+        if (mine) {
+            ok = __all_sync(0xffffffffu, rows_wait(&B.o_full[w], on & 1u, B, p.wait_ns));
+            ++on;
+            if (!ok) break;
+            tm_fence_after();
+        }
+        // a list that is whole in this segment (and has nothing to be joined with) becomes outputs here; where
+        // its units went to both warpgroups in turn, the second hands its record to the first
+        const bool whole = p.n_own == 0 && s.v0 == 0 && s.v1 == s.per;
+        const bool joint = whole && !s.both && s.per > 1;
+        const long long slot = rows_slot(p, cta, s.item, s.v0 == 0);
+        if (w == 1 && pending && (joint || !whole)) {   // the first warpgroup has read the record before it is written again
+            ok = __all_sync(0xffffffffu, rows_wait(&B.read, rn & 1, B, p.wait_ns));
+            ++rn;
+            if (!ok) break;
+            pending = false;
+        }
+        if (whole && !(joint && w == 1)) {
+            float f = 1.0f, f1 = 0.0f;
+            const float *other = p.rec + rows_rec(slot, 1, r) * rec_stride(D);
+            if (joint) {
+                ok = __all_sync(0xffffffffu, rows_wait(&B.join, jn & 1, B, p.wait_ns));
+                ++jn;
+                if (!ok) break;
+                if (valid) {
+                    const float m1 = __ldcg(other), l1 = __ldcg(other + 1), to = fmaxf(m, m1), base = to == -INFINITY ? 0.0f : to;
+                    f = exp2f(m - base);
+                    f1 = exp2f(m1 - base);
+                    l = l * f + l1 * f1;
+                }
+            }
+            if (any && mine) {
+                const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+                f *= inv;
+                f1 *= inv;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    tm_ld16(tO + 16 * c, o);
+                    tm_ready16(o);
+                    if (valid) {
+                        float y[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * f;
+                        if (joint) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 x = __ldcg(reinterpret_cast<const float4 *>(other + kRecHead + 16 * c) + i);
+                                y[4 * i] = fmaf(x.x, f1, y[4 * i]);
+                                y[4 * i + 1] = fmaf(x.y, f1, y[4 * i + 1]);
+                                y[4 * i + 2] = fmaf(x.z, f1, y[4 * i + 2]);
+                                y[4 * i + 3] = fmaf(x.w, f1, y[4 * i + 3]);
+                            }
+                        }
+                        if (p.out_dtype == DQK_BF16) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + at * D + 16 * c);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                                    pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + at * D + 16 * c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            __syncwarp();
+            if (joint && lane == 0) mbar_arrive(&B.read);
+        } else if (s.own || slot < p.rec_slots) {
+            float *rec = (s.own ? p.own_rec + rows_own_rec(cta + s.item, w, p.G, r) * rec_stride(D)
+                                : p.rec + rows_rec(slot, w, r) * rec_stride(D));
+            if (any) {
+                if (valid) {
+                    rec[0] = m;
+                    rec[1] = l;
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    if (mine) {
+                        tm_ld16(tO + 16 * c, o);
+                        tm_ready16(o);
+                    }
+                    if (valid) {
+                        float4 *dst = reinterpret_cast<float4 *>(rec + kRecHead + 16 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // no unit of this segment: an empty record
+                            dst[i] = mine ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (joint) {   // w == 1
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.join);
+                pending = true;
+            }
+        } else if (r == 0) {   // groups that overlap
+            dqk_flag_error(kErrBounds);
+        }
+        tm_fence_before();   // the accumulator has been read before the next segment's first product
+        n += s.both ? 2 * units : units;
+        unit0 += units;
+    }
+}
+
+template <int D, int kFmt, int NS, bool VCH0>
+__global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
+    k_rows(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap map) {
+    using T = RowsShape<D, kFmt>;
+    extern __shared__ __align__(1024) unsigned char rows_smem[];
+    unsigned char *tiles = rows_smem + ((1024u - (smem_addr(rows_smem) & 1023u)) & 1023u);
+    unsigned char *qmem = tiles + (size_t)(p.ktiles + p.vtiles) * T::kTile;
+    unsigned char *raw = qmem + 2 * T::kParts * T::kTile;
+    __shared__ RowsBars B;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRowsMaxTiles; ++i) {
+            mbar_init(&B.full[i], T::kFullCount);
+            mbar_init(&B.empty[i], 2);
+        }
+        for (int i = 0; i < kRowsFlags; ++i) mbar_init(&B.v_full[i], 1);
+        for (int i = 0; i < kRowsMaxRaw; ++i) {
+            mbar_init(&B.raw_full[i], 1);
+            mbar_init(&B.raw_empty[i], kRowsUnpackWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.q_full[i], 4);
+            mbar_init(&B.o_step[i], 1);
+            mbar_init(&B.o_full[i], 1);
+            mbar_init(&B.done[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&B.s_full[i][h], 1);
+                mbar_init(&B.p_full[i][h], 4);
             }
         }
-        if (ok) rows_record<D, kFmt>(p, s, (int)blockIdx.x, share, wm, rb, st, lane);
+        mbar_init(&B.join, 4);
+        mbar_init(&B.read, 4);
+        B.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        const RowsCursor c = rows_cursor(p, blockIdx.x, lane);
+        if (lane == 0) B.cursor = c;
+    }
+    if (warp == 9) tm_alloc(&B.tmem, 512);
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    const uint32_t tmem = B.tmem;
+    if (warp < 8) {
+        rows_softmax<D, kFmt>(p, B, qmem, tmem, warp >> 2, blockIdx.x);
+    } else {
+        if (warp == 8) rows_producer<D, kFmt>(p, &map, B, tiles, raw, lane);
+        else if (warp < 11) {
+            if (elect_one()) rows_matrix<D, kFmt>(p, B, tiles, qmem, tmem, warp - 9);
+            __syncwarp();
+        } else if constexpr (!T::kInt2) {
+            rows_tails<D>(p, B, tiles, lane);
+        } else {
+            if (warp >= 12) rows_unpack<D, NS, VCH0>(p, B, tiles, raw, warp - 12, lane);
+        }
     }
     grid_dependents_launch();
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    if (warp == 9) tm_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
 // merge: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the records of
-// the row head's group item and own item, in unit order; 0 without any token.
-// A warp per row head.
+// the row head's group item and own item, in order; 0 without any token.
 // ---------------------------------------------------------------------------
-constexpr int kRowsMergeWarps = 8;
-
 template <int D>
-__global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __grid_constant__ RowsParams p) {
-    constexpr int V = D / 32, kBatch = 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long head = (long long)blockIdx.x * kRowsMergeWarps + warp;   // row * hq + h
-    grid_dependency_wait();
-    const int row = (int)(head / p.hq), h = (int)(head - (long long)row * p.hq), j = h / p.G, hh = h - j * p.G;
-    if (row >= p.total_rows) return;
-    // the group of the row: the last one that starts at or before it
-    int g = -1;
-    for (int i0 = 0; i0 < p.n_groups; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < p.n_groups && rows_first(p, i) <= row && row < rows_first(p, i + 1);
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (m) {
-            g = i0 + __ffs(m) - 1;
-            break;
-        }
-    }
-    if (g < 0 && p.n_own == 0) return;   // behind the last sequence: left as it was
-    long long Ug, tiles_all;
-    rows_before_group(p, p.n_groups, lane, Ug, tiles_all);
-    const long long U = Ug + rows_before_own(p, p.n_own, lane);
-    const int C = p.num_ctas;
-    float M = -INFINITY, Ls = 0.0f, O[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) O[e] = 0.0f;
-    // record i of a part: CTA cf + i / shares, share i % shares
-    auto take = [&](bool own, long long ua, int per, long long item, int wm, int r) {
+struct RowsMerge {
+    static constexpr int V = D / 32, kBatch = 8;
+    float M = -INFINITY, L = 0.0f, O[V] = {};
+    // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose weighted units start
+    // at `start`: CTAs cf .. cl, both warpgroups' where the units went to one and the other.
+    __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, int both, long long q,
+                                         long long item, int r, int lane) {
         if (per <= 0) return;
-        const int cf = (int)cta_of_unit(ua, U, C), cl = (int)cta_of_unit(ua + per - 1, U, C);
-        const int shares = kRowsWarps / wm, n = (cl - cf + 1) * shares;
+        const int w = both ? 2 : 1, shares = both ? 1 : 2;
+        const int cf = (int)rows_div(start, q), cl = (int)rows_div(start + (long long)(per - 1) * w, q), n = (cl - cf + 1) * shares;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kBatch) {
             float m[kBatch], l[kBatch], o[kBatch][V];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int i = i0 + q, c = cf + i / shares;
-                m[q] = -INFINITY;
-                l[q] = 0.0f;
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k;
+                const long long c = cf + i / shares;
+                m[k] = -INFINITY;
+                l[k] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < V; ++e) o[q][e] = 0.0f;
-                if (i < n && (long long)c * U / C < ((long long)c + 1) * U / C && (own || c + item < p.rec_slots)) {
-                    const float *rec = own ? p.own_rec + rows_own_rec(c + item, i % shares, p.G, r) * rec_stride(D)
-                                           : p.rec + rows_rec(c + item, i % shares, wm, r) * rec_stride(D);
-                    m[q] = __ldcg(rec);
-                    l[q] = __ldcg(rec + 1);
+                for (int e = 0; e < V; ++e) o[k][e] = 0.0f;
+                // (a CTA with an odd range of one weighted unit may hold no start of a unit of weight 2)
+                const bool has = ceil_half(max(c * q - start, 0LL), w) < ceil_half(min((c + 1) * q - start, (long long)per * w), w);
+                const long long slot = rows_slot(p, c, item, c == cf);
+                if (i < n && has && (own || slot < p.rec_slots)) {
+                    const int g = both ? r >> 7 : i & 1, rr = both ? r & 127 : r;
+                    const float *rec = own ? p.own_rec + rows_own_rec(c + item, g, p.G, rr) * rec_stride(D)
+                                           : p.rec + rows_rec(slot, g, rr) * rec_stride(D);
+                    m[k] = __ldcg(rec);
+                    l[k] = __ldcg(rec + 1);
                     if constexpr (V == 4) {
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(rec + kRecHead) + lane);
-                        o[q][0] = x.x; o[q][1] = x.y; o[q][2] = x.z; o[q][3] = x.w;
+                        o[k][0] = x.x; o[k][1] = x.y; o[k][2] = x.z; o[k][3] = x.w;
                     } else {
                         const float2 x = __ldcg(reinterpret_cast<const float2 *>(rec + kRecHead) + lane);
-                        o[q][0] = x.x; o[q][1] = x.y;
+                        o[k][0] = x.x; o[k][1] = x.y;
                     }
                 }
             }
-            float Mn = M;
+            float to = M;
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) Mn = fmaxf(Mn, m[q]);
-            const float base = Mn == -INFINITY ? 0.0f : Mn;
-            const float sc = exp2f(M - base);   // 0 while M is -inf
-            Ls *= sc;
+            for (int k = 0; k < kBatch; ++k) to = fmaxf(to, m[k]);
+            const float base = to == -INFINITY ? 0.0f : to, sc = exp2f(M - base);   // 0 while M is -inf
+            M = to;
+            L *= sc;
 #pragma unroll
             for (int e = 0; e < V; ++e) O[e] *= sc;
-            M = Mn;
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const float w = exp2f(m[q] - base);   // 0 for an empty record, whose o holds zeros
-                Ls = fmaf(w, l[q], Ls);
+            for (int k = 0; k < kBatch; ++k) {
+                const float f = exp2f(m[k] - base);   // 0 for an empty record, whose o holds zeros
+                L = fmaf(f, l[k], L);
 #pragma unroll
-                for (int e = 0; e < V; ++e) O[e] = fmaf(w, o[q][e], O[e]);
+                for (int e = 0; e < V; ++e) O[e] = fmaf(f, o[k][e], O[e]);
             }
         }
-    };
-    if (g >= 0) {
-        long long before, tiles;
-        rows_before_group(p, g, lane, before, tiles);
-        const int first = rows_first(p, g), per = rows_units(rows_len(p.kv_lens, g, p.max_pages));
-        const int rr = (row - first) * p.G + hh, mt = rr / kRowsTile, r = rr - mt * kRowsTile;
-        const int nr = min(kRowsTile, (rows_first(p, g + 1) - first) * p.G - mt * kRowsTile);
-        const int k = mt * p.hkv + j;
-        take(false, before + (long long)k * per, per, tiles * p.hkv + k, rows_blocks(nr), r);
     }
-    if (p.n_own > 0) {
-        const int per = rows_units(rows_len(p.own_lens, row, p.own_max_pages));
-        const long long ua = Ug + rows_before_own(p, row, lane) + (long long)j * per;
-        take(true, ua, per, (long long)row * p.hkv + j, 1, hh);
-    }
-    const float inv = Ls != 0.0f ? 1.0f / Ls : 0.0f;
-    const size_t at = (size_t)head * D + V * lane;
-    if (p.out_dtype == DQK_BF16) {
-        uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + at;
-        if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(O[0] * inv, O[1] * inv);
-    } else {
-        float *out = reinterpret_cast<float *>(p.out) + at;
+    __device__ __forceinline__ void store(const RowsParams &p, size_t head, int lane) const {
+        const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+        const size_t at = head * D + V * lane;
+        if (p.out_dtype == DQK_BF16) {
+            uint16_t *out = reinterpret_cast<uint16_t *>(p.out) + at;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2 *>(out) =
+                    make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(O[0] * inv, O[1] * inv);
+        } else {
+            float *out = reinterpret_cast<float *>(p.out) + at;
 #pragma unroll
-        for (int e = 0; e < V; ++e) out[e] = O[e] * inv;
+            for (int e = 0; e < V; ++e) out[e] = O[e] * inv;
+        }
+    }
+};
+
+constexpr int kRowsMergeWarps = 8, kRowsMergeHeads = 16, kRowsMergeRows = 32;
+
+// With own lists (decode): CTA = (query row, up to 16 of its heads), a warp per head, over the records of its
+// group's item and its own.
+template <int D>
+__global__ void __launch_bounds__(32 * kRowsMergeHeads) k_rows_merge(const __grid_constant__ RowsParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int row = blockIdx.x, h = blockIdx.y * warps + warp;
+    __shared__ long long sh_q, sh_before, sh_tile0, sh_own;
+    __shared__ int sh_group;
+    grid_dependency_wait();
+    if (warp == 0) {
+        long long U, tiles;
+        rows_sums(p, p.n_groups + p.n_own, lane, U, tiles);
+        if (lane == 0) sh_q = rows_share(U, p.num_ctas);
+    }
+    if (warp == 1 % warps) {
+        int g = -1;
+        long long before = 0, tile0 = 0;
+        for (int i0 = 0; i0 < p.n_groups; i0 += 32) {
+            const int i = i0 + lane;
+            const unsigned hit =
+                __ballot_sync(0xffffffffu, i < p.n_groups && rows_first(p, i) <= row && row < rows_first(p, i + 1));
+            if (hit) {
+                g = i0 + __ffs(hit) - 1;
+                break;
+            }
+        }
+        if (g >= 0) rows_sums(p, g, lane, before, tile0);
+        if (lane == 0) {
+            sh_group = g;
+            sh_before = before;
+            sh_tile0 = tile0;
+        }
+    }
+    if (warp == 2 % warps) {
+        long long before, tiles;
+        rows_sums(p, p.n_groups + row, lane, before, tiles);
+        if (lane == 0) sh_own = before;
+    }
+    __syncthreads();
+    if (h >= p.hq) return;
+    const int j = h / p.G, hh = h - j * p.G, g = sh_group;
+    const long long q = sh_q;
+    RowsMerge<D> acc;
+    if (g >= 0) {
+        const RowsList r = rows_list(p, g);
+        const int rr = (row - rows_first(p, g)) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? 2 : r.last;
+        acc.take(p, false, sh_before + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, r.per, w == 2, q,
+                 (sh_tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
+    }
+    const int per = rows_list(p, p.n_groups + row).per;
+    acc.take(p, true, sh_own + (long long)j * per, per, 0, q, (long long)row * p.hkv + j, hh, lane);
+    acc.store(p, (size_t)row * p.hq + h, lane);
+}
+
+// Without own lists, CTA (b, y): row heads 32 y .. 32 y + 31 of the item that begins in CTA b of the row kernel and
+// goes on in the next one (every other item's outputs are written already); the CTAs behind those zero the rows of
+// groups without any token.
+template <int D>
+__global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const __grid_constant__ RowsParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    grid_dependency_wait();
+    if (b >= p.num_ctas - 1) {
+        for (int g = b - (p.num_ctas - 1); g < p.n_groups; g += (int)gridDim.x - (p.num_ctas - 1)) {
+            if (rows_list(p, g).per > 0) continue;
+            const size_t at = (size_t)rows_first(p, g) * p.hq * D, n = (size_t)max(rows_first(p, g + 1) - rows_first(p, g), 0) * p.hq * D;
+            const RowsMerge<D> zero;
+            for (size_t x = (size_t)blockIdx.y * kRowsMergeWarps + warp; x < n / D; x += (size_t)gridDim.y * kRowsMergeWarps)
+                zero.store(p, at / D + x, lane);
+        }
+        return;
+    }
+    const RowsCursor c = rows_cursor(p, b + 1, lane);
+    if (c.u0 >= c.u1) return;
+    const RowsList r = rows_list(p, c.list);
+    const int mt = c.k / p.hkv, j = c.k - mt * p.hkv, w = mt < r.tiles - 1 ? 2 : r.last;
+    const long long start = c.first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, q = rows_div(c.u0, b + 1);
+    if (start >= c.u0 || rows_div(start, q) != b || start + (long long)(r.per - 1) * w < c.u0) return;
+    const int first = rows_first(p, c.list), nr = min(kRowsTile, (rows_first(p, c.list + 1) - first) * p.G - mt * kRowsTile);
+    for (int x = blockIdx.y * kRowsMergeRows + warp; x < min(nr, (int)(blockIdx.y + 1) * kRowsMergeRows); x += kRowsMergeWarps) {
+        const int rr = mt * kRowsTile + x;
+        RowsMerge<D> acc;
+        acc.take(p, false, start, r.per, w == 2, q, 0, x, lane);
+        acc.store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)j * p.G + rr % p.G, lane);
     }
 }
 

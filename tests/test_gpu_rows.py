@@ -234,3 +234,45 @@ def test_offsets_past_32_bits():
         check_prefix(L, queries(L, 2), "bf16", [0, 2])
         del L
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (128, "f32"), (64, "bf16")])
+def test_many_short_lists_per_block(d, dtype):
+    """Dozens of whole lists and a few split ones on every block: items that end
+    inside a block hand records between its warpgroups, the others go through
+    the merge."""
+    rng = np.random.default_rng(8)
+    nkv = rng.integers(0, 700, 150).tolist()
+    nq = rng.integers(0, 4, 150).tolist()
+    nq[7], nkv[7], nq[20], nkv[20] = 90, 650, 150, 300
+    L = R.Lists("bf16", [nkv], 8, 4, d, dtype=dtype, seed=16)
+    start = np.concatenate([[0], np.cumsum(nq)])
+    q = queries(L, int(start[-1]))
+    out = L.cross(q, dtype, start.tolist(), "bf16")
+    assert Q.dqk_last_device_error() == Q.DQK_OK
+    for b in range(len(nq)):
+        for r in range(start[b], start[b + 1], 1 if nq[b] < 10 else 17):
+            ref, bound = L.attend(L.query(q[r], dtype, 0)[0], [L.rows[0][b]], dtype, "bf16")
+            R.check(out[r], ref, bound, f"row {r}")
+
+
+@pytest.mark.parametrize("cache", ["int2", "bf16"])
+def test_references_that_move(cache):
+    """Scores that grow along the list: the running reference of nearly every
+    row moves many times, by more than its slack."""
+    L = R.Lists(cache, [[900, 260], [150, 300, 0, 64, 5]], 8, 2, 128, seed=17)
+    q = queries(L, 5, scale=0.1)
+    if cache == "bf16":
+        # keys along one direction, growing with the token
+        blk = L.pool.view(torch.bfloat16).view(L.num_pages, 2, 2, 16, 128)
+        for i, (table, lens) in enumerate(zip(L.tables, L.lens_list)):
+            for g, n in enumerate(lens):
+                for t in range(n):
+                    for j in range(2):
+                        x = torch.full((128,), 0.02 * (t + 300 * i), dtype=torch.bfloat16, device=L.dev)
+                        blk[int(table[g, t // 16]), j, 0, t % 16] = x      # equal channels: chunk order does not matter
+                        L.rows[i][g][0][t, j] = float(x[0])
+        q = np.abs(q) + 0.05
+    else:
+        q = q * 60.0
+    check_prefix(L, q, "f32", [0, 3, 5])
