@@ -141,12 +141,11 @@ __device__ __forceinline__ void rows_sums(const RowsParams &p, int n, int lane, 
     tiles = t;
 }
 
-// Walks the segments -- stretches of one item's units -- of a CTA in order.
+// The start of a CTA's walk: its weighted units [u0, u1), the item that holds u0 (first weighted
+// unit `start`), and the row tiles of the groups before its list.
 struct RowsCursor {
-    long long u0, u1;       // the CTA's weighted units
-    long long first;        // first weighted unit of the list
-    long long tile0;        // row tiles of the groups before it
-    int list, k;            // list, next (tile, kv head) of it
+    long long u0, u1, start, tile0;
+    int list, mt, j;
 };
 
 // Weighted units per CTA (and the general quotient: 32-bit division where it fits).
@@ -161,7 +160,7 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
     // one pass when every list has a lane, else the sums first
     long long U = 0, tiles = 0, base = 0, tbase = 0;
     if (n > 32) rows_sums(p, n, lane, U, tiles);
-    RowsCursor c{0, 0, 0, 0, n, 0};
+    RowsCursor c{0, 0, 0, 0, n, 0, 0};
     for (int i0 = 0; i0 < n; i0 += 32) {
         const int i = i0 + lane;
         RowsList r{0, 1, 0, 0};
@@ -178,16 +177,22 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
         const bool hit = r.units > 0 && base + ui - r.units <= c.u0 && c.u0 < base + ui;
         const unsigned m = __ballot_sync(0xffffffffu, hit);
         if (m) {
-            int k = 0;   // the (tile, kv head) that holds u0
+            int mt = 0, j = 0;   // the (tile, kv head) that holds u0
+            long long start = 0;
             if (hit) {
-                const long long local = c.u0 - (base + ui - r.units), full = (long long)(r.tiles - 1) * p.hkv * r.per * 2;
-                k = local < full ? (int)rows_div(local, 2LL * r.per) : (r.tiles - 1) * p.hkv + (int)rows_div(local - full, (long long)r.last * r.per);
+                const long long first = base + ui - r.units, local = c.u0 - first, full = (long long)(r.tiles - 1) * p.hkv * r.per * 2;
+                const int w = local < full ? 2 : r.last;
+                const int k = (int)rows_div(local < full ? local : local - full, (long long)w * r.per);
+                mt = local < full ? k / p.hkv : r.tiles - 1;
+                j = local < full ? k - mt * p.hkv : k;
+                start = first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w;
             }
             const int src = __ffs(m) - 1;
             c.list = i0 + src;
-            c.first = base + __shfl_sync(0xffffffffu, ui - r.units, src);
+            c.start = __shfl_sync(0xffffffffu, start, src);
             c.tile0 = tbase + __shfl_sync(0xffffffffu, ti - (i < p.n_groups ? r.tiles : 0), src);
-            c.k = __shfl_sync(0xffffffffu, k, src);
+            c.mt = __shfl_sync(0xffffffffu, mt, src);
+            c.j = __shfl_sync(0xffffffffu, j, src);
             break;
         }
         base += __shfl_sync(0xffffffffu, ui, 31);
@@ -196,48 +201,75 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
     return c;
 }
 
-struct RowsSeg {
-    int own, list;          // own list, or group
-    int j, both;            // kv head; both warpgroups take every unit (tile of more than 128 row heads)
-    int row0, rbase, nr;    // first query row of the list, first row head of the tile, row heads in it
-    int len, per, v0, v1;   // tokens and units of the list, units [v0, v1) of this segment
-    long long item;         // record slot: CTA + item
-};
-
 __device__ __forceinline__ long long ceil_half(long long x, int w) { return w == 2 ? (x + 1) >> 1 : x; }
 
-__device__ __noinline__ bool rows_next(const RowsParams &p, RowsCursor &c, RowsSeg &s) {
-    while (c.list < p.n_groups + p.n_own) {
-        const RowsList r = rows_list(p, c.list);
-        if (r.units == 0 || c.k >= r.tiles * p.hkv) {
-            c.first += r.units;
-            c.tile0 += c.list < p.n_groups ? r.tiles : 0;
-            ++c.list;
-            c.k = 0;
-            continue;
+// Walks the segments -- stretches [v0, v1) of one item's units -- of a CTA in order.
+struct RowsWalk {
+    long long start, u1, tile0;     // the item's first weighted unit, the CTA's end, row tiles of the groups before
+    int list, tiles, last, per, len, row0, heads;   // the list: shape, tokens, first query row, row heads
+    int mt, j, w;                   // the item: row tile, kv head, weight
+    int v0, v1;
+    bool live;
+    __device__ __forceinline__ void load(const RowsParams &p) {
+        const RowsList r = rows_list(p, list);
+        tiles = r.tiles;
+        last = r.last;
+        per = r.per;
+        if (list < p.n_groups) {
+            row0 = rows_first(p, list);
+            heads = (rows_first(p, list + 1) - row0) * p.G;
+            len = rows_len(p.kv_lens, list, p.max_pages);
+        } else {
+            row0 = list - p.n_groups;
+            heads = p.G;
+            len = rows_len(p.own_lens, row0, p.own_max_pages);
         }
-        const int mt = c.k / p.hkv, w = mt < r.tiles - 1 ? 2 : r.last;
-        const long long start = c.first + (long long)mt * p.hkv * r.per * 2 + (long long)(c.k - mt * p.hkv) * r.per * w;
-        if (start >= c.u1) return false;
-        s.v0 = (int)ceil_half(max(c.u0 - start, 0LL), w);
-        s.v1 = (int)ceil_half(min(c.u1 - start, (long long)r.per * w), w);
-        const bool own = c.list >= p.n_groups;
-        const int i = own ? c.list - p.n_groups : c.list;
-        s.own = own;
-        s.list = i;
-        s.j = c.k - mt * p.hkv;
-        s.both = w == 2;
-        s.row0 = own ? i : rows_first(p, i);
-        s.rbase = mt * kRowsTile;
-        s.nr = own ? p.G : min(kRowsTile, (rows_first(p, i + 1) - s.row0) * p.G - s.rbase);
-        s.len = own ? rows_len(p.own_lens, i, p.own_max_pages) : rows_len(p.kv_lens, i, p.max_pages);
-        s.per = r.per;
-        s.item = own ? (long long)i * p.hkv + s.j : c.tile0 * p.hkv + c.k;
-        ++c.k;
-        if (s.v0 < s.v1) return true;
     }
-    return false;
-}
+    __device__ __forceinline__ void begin(const RowsParams &p, const RowsCursor &c) {
+        list = c.list;
+        live = c.u0 < c.u1 && list < p.n_groups + p.n_own;
+        if (!live) return;
+        load(p);
+        start = c.start;
+        u1 = c.u1;
+        tile0 = c.tile0;
+        mt = c.mt;
+        j = c.j;
+        w = mt < tiles - 1 ? 2 : last;
+        v0 = (int)ceil_half(c.u0 - start, w);
+        v1 = (int)ceil_half(min(u1 - start, (long long)per * w), w);
+        if (v0 >= v1) next(p);   // the CTA's only unit of it starts one earlier
+    }
+    __device__ __forceinline__ void next(const RowsParams &p) {
+        start += (long long)per * w;
+        if (++j == p.hkv) {
+            j = 0;
+            if (++mt == tiles) {
+                do {
+                    if (list < p.n_groups) tile0 += tiles;
+                    if (++list >= p.n_groups + p.n_own) {
+                        live = false;
+                        return;
+                    }
+                    load(p);
+                } while (tiles == 0 || per == 0);
+                mt = 0;
+            }
+            w = mt < tiles - 1 ? 2 : last;
+        }
+        live = start < u1;
+        v0 = 0;
+        v1 = live ? (int)ceil_half(min(u1 - start, (long long)per * w), w) : 0;
+    }
+    __device__ __forceinline__ bool own(const RowsParams &p) const { return list >= p.n_groups; }
+    __device__ __forceinline__ bool both() const { return w == 2; }   // both warpgroups take every unit
+    __device__ __forceinline__ int units() const { return v1 - v0; }
+    __device__ __forceinline__ int rows() const { return min(kRowsTile, heads - mt * kRowsTile); }
+    // record slot: CTA + item
+    __device__ __forceinline__ long long item(const RowsParams &p) const {
+        return own(p) ? (long long)row0 * p.hkv + j : (tile0 + mt) * p.hkv + j;
+    }
+};
 
 // Record slots of the groups' items.  With own lists every segment is joined with another:
 // slot CTA + item (a CTA's segments are of consecutive items).  Without, only items that cross
@@ -545,30 +577,32 @@ struct RowsRing {
     }
 };
 
+// Pages of a unit that are multiplied, in pairs (a k-step of 16 tokens of a half): those before the list's end.
+__device__ __forceinline__ int rows_pairs(int nv) { return min((nv + 2 * kPage - 1) / (2 * kPage), kRowsPages / 2); }
+
 // The units of a CTA in order, for the matrix threads.
 struct RowsUnits {
-    RowsCursor cur;
-    RowsSeg s;
+    RowsWalk s;
     RowsRing k, t;     // places of the unit's key tile and of its value tile
     int v, n, unit;    // unit of the item, jobs and units before it
-    bool live;
     __device__ __forceinline__ void start(const RowsParams &p, const RowsCursor &c) {
-        cur = c;
         n = unit = 0;
-        live = rows_next(p, cur, s);
-        v = live ? s.v0 : 0;
+        s.begin(p, c);
+        v = s.live ? s.v0 : 0;
     }
-    __device__ __forceinline__ bool mine(int w) const { return s.both || ((n ^ w) & 1) == 0; }
-    __device__ __forceinline__ bool first() const { return s.both ? v == s.v0 : v < s.v0 + 2; }   // of a warpgroup's in the segment
-    __device__ __forceinline__ bool last() const { return s.both ? v == s.v1 - 1 : v >= s.v1 - 2; }
+    __device__ __forceinline__ bool live() const { return s.live; }
+    __device__ __forceinline__ bool mine(int w) const { return s.both() || ((n ^ w) & 1) == 0; }
+    // the first, the last of a warpgroup's units in the segment
+    __device__ __forceinline__ bool first() const { return s.both() ? v == s.v0 : v < s.v0 + 2; }
+    __device__ __forceinline__ bool last() const { return s.both() ? v == s.v1 - 1 : v >= s.v1 - 2; }
     __device__ __forceinline__ void next(const RowsParams &p) {
-        n += s.both ? 2 : 1;
+        n += s.w;
         ++unit;
         k.next(p.ktiles);
         t.next(p.vtiles);
         if (++v == s.v1) {
-            live = rows_next(p, cur, s);
-            v = live ? s.v0 : 0;
+            s.next(p);
+            v = s.v0;
         }
     }
 };
@@ -598,16 +632,15 @@ template <int D, int kFmt>
 __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtensorMap *map, RowsBars &B, unsigned char *tiles,
                                               unsigned char *raw, int lane) {
     using T = RowsShape<D, kFmt>;
-    RowsCursor cur = B.cursor;
-    RowsSeg s;
+    RowsWalk s;
     RowsRing ring[2];   // raw blocks, or key and value tiles
     int unit = 0;
     bool ok = true;
     const int pg = lane & (kRowsPages - 1), h = lane >> 3;   // lanes 0 .. 7 copy a page each
-    while (ok && rows_next(p, cur, s)) {
-        const int *tab = s.own ? p.own_table + (size_t)s.list * p.own_max_pages : p.table + (size_t)s.list * p.max_pages;
+    for (s.begin(p, B.cursor); ok && s.live; s.next(p)) {
+        const int *tab = s.own(p) ? p.own_table + (size_t)s.row0 * p.own_max_pages : p.table + (size_t)s.list * p.max_pages;
         const int npages = (s.len + kPage - 1) / kPage;
-        if (lane == 0 && (s.own ? p.own_lens[s.list] : p.kv_lens[s.list]) > s.len) dqk_flag_error(kErrBounds);
+        if (lane == 0 && (s.own(p) ? p.own_lens[s.row0] : p.kv_lens[s.list]) > s.len) dqk_flag_error(kErrBounds);
         int page = s.v0 * kRowsPages + pg;
         int phys = page < npages ? tab[page] : -1;
         for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
@@ -670,13 +703,12 @@ template <int D, int NS, bool VCH0>
 __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *raw, int warp,
                                             int lane) {
     constexpr int kTile = kRowsKv * D * 2;
-    RowsCursor cur = B.cursor;
-    RowsSeg s;
+    RowsWalk s;
     RowsRing rr, rk, rv;
     int unit = 0;
     bool ok = true;
     const int mi = lane >> 3, r8 = lane & 7, tig = lane & 3;
-    while (ok && rows_next(p, cur, s)) {
+    for (s.begin(p, B.cursor); ok && s.live; s.next(p)) {
         for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
             const int rs = rr.st;
             ok = rows_wait(&B.raw_full[rs], rr.phase, B, p.wait_ns);
@@ -691,7 +723,7 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
             const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
             const uint32_t kt = smem_addr(tiles) + (uint32_t)sk * kTile, vt = smem_addr(tiles) + (uint32_t)sv * kTile;
 #pragma unroll 1
-            for (int pg = warp; pg < kRowsPages; pg += kRowsUnpackWarps) {
+            for (int pg = warp; pg < 2 * rows_pairs(s.len - v * kRowsKv); pg += kRowsUnpackWarps) {
                 // rows of the matrix this lane addresses: keys, token 8 (mi >> 1) + r8 of the page, column chunk
                 // 2s + (mi & 1); values, channel 16m + 8 (mi >> 1) + r8, the page's tokens of half mi & 1
                 const uint32_t ka = kt + (uint32_t)(64 * (mi >> 1) + 8 * pg + r8) * 128;
@@ -750,26 +782,28 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
 // brought stale memory, or nothing, there) before the tile's first use.
 template <int D>
 __device__ __forceinline__ void rows_tails(const RowsParams &p, RowsBars &B, unsigned char *tiles, int lane) {
-    constexpr int kChunks = D / 8, kTile = kRowsKv * D * 2;
-    RowsCursor cur = B.cursor;
-    RowsSeg s;
+    constexpr int kChunks = D / 8, kTile = kRowsKv * D * 2, kRowStep = 32 / kChunks;   // rows a warp zeros at once
+    RowsWalk s;
     RowsRing ring;
     int unit = 0;
     bool ok = true;
-    while (ok && rows_next(p, cur, s)) {
+    for (s.begin(p, B.cursor); ok && s.live; s.next(p)) {
         for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
             ok = __all_sync(0xffffffffu, rows_wait(&B.full[p.ktiles + ring.st], ring.phase, B, p.wait_ns));
             if (!ok) break;
             const int nv = s.len - v * kRowsKv;
             const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
             if (nv < kRowsKv || have != (1u << kRowsPages) - 1u) {
-                const uint32_t tile = smem_addr(tiles) + (uint32_t)(p.ktiles + ring.st) * kTile;
-                const int from = have == (1u << kRowsPages) - 1u ? nv : 0;   // all pages there: the rows behind the end
-                for (int i = from * kChunks + lane; i < kRowsKv * kChunks; i += 32) {
-                    const int row = i / kChunks, c = i % kChunks, pg = row >> 4;
-                    if (row >= nv || !((have >> pg) & 1u))
-                        st_s128(tile + (uint32_t)(pg * (kPage * D * 2) + (c >> 3) * (kPage * 128) + (row & 15) * 128 + (c & 7) * 16),
-                                make_uint4(0u, 0u, 0u, 0u));
+                const int c = lane % kChunks, r0 = lane / kChunks;
+                const uint32_t at = smem_addr(tiles) + (uint32_t)(p.ktiles + ring.st) * kTile +
+                                    (uint32_t)((c >> 3) * (kPage * 128) + (c & 7) * 16);
+#pragma unroll 1
+                for (int pg = 0; pg < 2 * rows_pairs(nv); ++pg) {
+                    const int n = (have >> pg) & 1u ? nv - kPage * pg : 0;   // rows of the page that stay
+                    if (n >= kPage) continue;
+#pragma unroll
+                    for (int r = 0; r < kPage; r += kRowStep)
+                        if (r + r0 >= n) st_s128(at + (uint32_t)(pg * (kPage * D * 2) + (r + r0) * 128), make_uint4(0u, 0u, 0u, 0u));
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -796,7 +830,7 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
     bool key_seen = false;      // of a unit to be passed over: its key tile is released
     // Moves nx on; false: not there yet (a tile to be passed over has not landed), or abort.
     auto seek = [&](bool block) {
-        while (nx.live && !nx.mine(w)) {
+        while (nx.live() && !nx.mine(w)) {
             const int kt = nx.k.st, vt = p.ktiles + nx.t.st;
             if (!key_seen) {
                 if (!(block ? rows_wait(&B.full[kt], nx.k.phase, B, p.wait_ns) : mbar_test_wait(&B.full[kt], nx.k.phase))) return false;
@@ -833,7 +867,7 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
         return rows_wait(&B.full[nx.k.st], nx.k.phase, B, p.wait_ns);
     };
     ok = seek(true);
-    if (ok && nx.live) {
+    if (ok && nx.live()) {
         ok = operands();
         if (ok) {
             tm_fence_after();
@@ -842,12 +876,13 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
             mma_commit(&B.empty[nx.k.st]);
         }
     }
-    while (ok && nx.live) {
+    while (ok && nx.live()) {
         // this job (nx moves on to the one after)
         const int vt = p.ktiles + nx.t.st, unit = nx.unit;
         const uint32_t vphase = nx.t.phase;
         const uint32_t acc = nx.first() ? 0u : 1u;
         const bool last = nx.last();
+        const int pairs = rows_pairs(nx.s.len - nx.v * kRowsKv);
         // BF16: rows of tokens, contiguous channels; INT2: rows of channels, contiguous tokens
         const uint32_t b = desc_low(tile0 + (uint32_t)vt * T::kTile, T::kInt2 ? 16 : kPage * 128);
         nx.next(p);
@@ -857,12 +892,13 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             // the next job's operands, if they are there (an item's queries are loaded after the item before is finished)
-            const bool early = h == 0 && ok && seek(false) && nx.live && !nx.first() && mbar_test_wait(&B.full[nx.k.st], nx.k.phase);
+            const bool early = h == 0 && ok && seek(false) && nx.live() && !nx.first() && mbar_test_wait(&B.full[nx.k.st], nx.k.phase);
             ok = ok && rows_wait(&B.p_full[w][h], pn, B, p.wait_ns);
             if (!ok) break;
             tm_fence_after();
 #pragma unroll
             for (int s = 0; s < kRowsKv / 32; ++s) {
+                if (s >= pairs) break;
                 const uint32_t off = (uint32_t)(T::kInt2 ? h * (D * 128) + s * 32 : 2 * s * T::kPageBytes + h * 1024) >> 4;
                 mma_ts<T::kGroupKv>(tO, tS + 64 * h + 8 * s, b + off, T::kIdescO, h > 0 || s > 0 ? 1u : acc);
             }
@@ -882,7 +918,7 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
         mma_commit(&B.empty[vt]);
         if (!ahead) {
             ok = seek(true);
-            if (ok && nx.live) {
+            if (ok && nx.live()) {
                 ok = operands();
                 if (!ok) break;
                 tm_fence_after();
@@ -1019,67 +1055,105 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, float qs, fl
     return true;
 }
 
-// Softmax warpgroup w: thread = row head.
+// A softmax thread's part in a segment: thread = row head.
+struct RowsPart {
+    size_t at;               // its row of q and out
+    int vf;                  // the warpgroup's units: vf, vf + step, ...
+    bool mine, valid, any;   // it has one; the thread has a row; its warp has
+};
+__device__ __forceinline__ RowsPart rows_part(const RowsParams &p, const RowsWalk &s, int n, int w, int r) {
+    RowsPart t;
+    const int rows = s.rows() - (s.both() ? kRowsHalf * w : 0), rr = s.mt * kRowsTile + (s.both() ? kRowsHalf * w : 0) + r;
+    t.vf = s.both() ? s.v0 : s.v0 + ((n ^ w) & 1);
+    t.mine = s.live && t.vf < s.v1;
+    t.valid = s.live && r < rows;
+    t.any = s.live && (r & ~31) < rows;
+    const int g = p.G == 8 ? 3 : p.G >> 1;   // log2 G
+    t.at = t.valid ? (size_t)(s.row0 + (rr >> g)) * p.hq + (size_t)s.j * p.G + (rr & (p.G - 1)) : 0;
+    return t;
+}
+
+// The thread's query row into its warpgroup's operand tile (asynchronously, unless it has to be split in parts).
+template <int D, int kFmt>
+__device__ __forceinline__ void rows_query(const RowsParams &p, const RowsPart &t, uint32_t tile, int r) {
+    using T = RowsShape<D, kFmt>;
+    if (!t.mine || !t.valid) return;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        const uint32_t dst = tile + (uint32_t)(r * 128 + (c >> 3) * (kRowsKv * 128) + (((c & 7) ^ (r & 7)) << 4));
+        if constexpr (kFmt != 1) {
+            cp_async16(dst, reinterpret_cast<const uint16_t *>(p.q) + t.at * D + 8 * c);
+        } else {
+            const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + t.at * D + 8 * c);
+            const float4 a = f[0], b = f[1];
+            const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                lo[i] = pack_bf16x2(x[2 * i] - __uint_as_float(hi[i] << 16), x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
+            }
+            st_s128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_s128(dst + T::kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+    }
+}
+
+// Softmax warpgroup w.
 template <int D, int kFmt>
 __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, unsigned char *qmem, uint32_t tmem, int w, int cta) {
     using T = RowsShape<D, kFmt>;
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16, qtile = smem_addr(qmem) + (uint32_t)(w * T::kParts * T::kTile);
     const uint32_t tS = tmem + lanes + T::kS0 + 128 * w, tO = tmem + lanes + T::kO0 + D * w;
-    RowsCursor cur = B.cursor;
-    RowsSeg s;
     int n = 0, unit0 = 0;                     // jobs and units before the segment
     uint32_t jobs = 0, pn = 0, on = 0, jn = 0, rn = 0;   // jobs and halves done; waits done on o_full, join, read
     bool ok = true, pending = false;          // pending (second warpgroup): a record the first has yet to read
-    while (ok && rows_next(p, cur, s)) {
-        const int units = s.v1 - s.v0;
-        const int step = s.both ? 1 : 2;                                  // this warpgroup's units: vf, vf + step, ...
-        const int vf = s.both ? s.v0 : s.v0 + ((n ^ w) & 1);
-        const int rows = s.both ? s.nr - kRowsHalf * w : s.nr;            // its row heads (r < rows)
-        const bool mine = vf < s.v1, valid = r < rows, any = 32 * quad < rows;
-        const int rr = s.rbase + (s.both ? kRowsHalf * w : 0) + r;
-        const size_t at = valid ? (size_t)(s.row0 + rr / p.G) * p.hq + (size_t)s.j * p.G + rr % p.G : 0;
+    RowsWalk s;
+    s.begin(p, B.cursor);
+    RowsPart t = rows_part(p, s, n, w, r);
+    auto queries_in = [&](const RowsPart &x) {
+        if (!x.mine) return;
+        if constexpr (kFmt != 1) cp_async_wait_all();
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.q_full[w]);
+    };
+    rows_query<D, kFmt>(p, t, qtile, r);
+    queries_in(t);
+    while (s.live) {
         float m = -INFINITY, l = 0.0f, qs = p.qs;
-        if (mine) {
-            if (valid) {
-                if constexpr (kFmt == 2) qs = p.q_scale[at];
-                const uint32_t row = smem_addr(qmem) + (uint32_t)(w * T::kParts * T::kTile) + (uint32_t)r * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t dst = row + (uint32_t)((c >> 3) * (kRowsKv * 128) + (((c & 7) ^ (r & 7)) << 4));
-                    if constexpr (kFmt != 1) {
-                        st_s128(dst, *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + at * D + 8 * c));
-                    } else {
-                        const float4 *f = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + at * D + 8 * c);
-                        const float4 a = f[0], b = f[1];
-                        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                            lo[i] = pack_bf16x2(x[2 * i] - __uint_as_float(hi[i] << 16),
-                                                x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
-                        }
-                        st_s128(dst, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        st_s128(dst + T::kTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    }
-                }
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.q_full[w]);
+        if constexpr (kFmt == 2) {
+            if (t.valid) qs = p.q_scale[t.at];
         }
-        for (int v = vf; ok && v < s.v1; v += step) {
+        const int step = s.both() ? 1 : 2;
+        RowsWalk sn;          // the next segment
+        RowsPart tn;
+        if (!t.mine) {
+            sn = s;
+            sn.next(p);
+            tn = rows_part(p, sn, n + s.w * s.units(), w, r);
+            rows_query<D, kFmt>(p, tn, qtile, r);
+        }
+        for (int v = t.vf; v < s.v1; v += step) {
             const int nv = s.len - v * kRowsKv;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h, ++pn) {
                 ok = __all_sync(0xffffffffu, rows_wait(&B.s_full[w][h], jobs & 1u, B, p.wait_ns));
-                if (!ok) break;
+                if (!ok) return;
                 tm_fence_after();
-                if (any) {   // warps whose 32 rows are all past the tile leave the weights as they are: rows do not mix
+                if (h && v + step >= s.v1) {
+                    // the last scores of the segment: its queries are not needed any more, the next segment's come
+                    // in while these scores become weights
+                    sn = s;
+                    sn.next(p);
+                    tn = rows_part(p, sn, n + s.w * s.units(), w, r);
+                    rows_query<D, kFmt>(p, tn, qtile, r);
+                }
+                if (t.any) {   // warps whose 32 rows are all past the tile leave the weights as they are: rows do not mix
                     const uint32_t have = B.flags[(unit0 + v - s.v0) & (kRowsFlags - 1)];
                     if (nv < kRowsKv || have != (1u << kRowsPages) - 1u) rows_mask(tS + 64 * h, nv, have, h);
-                    const bool none = v == vf && h == 0;
+                    const bool none = v == t.vf && h == 0;
                     if (none) m = ceilf(rows_largest(tS, qs));   // no reference yet
                     // the half before this one may still be on its way into the accumulator (the one before that is not:
                     // these scores lie where its weights were)
@@ -1089,7 +1163,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                         tm_fence_after();
                         return 1;
                     });
-                    if (!ok) break;
+                    if (!ok) return;
                 }
                 tm_fence_before();
                 __syncwarp();
@@ -1097,22 +1171,23 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             }
             ++jobs;
         }
-        if (!ok) break;
-        if (mine) {
+        // the next segment's scores are formed while this one's accumulator is read
+        queries_in(tn);
+        if (t.mine) {
             ok = __all_sync(0xffffffffu, rows_wait(&B.o_full[w], on & 1u, B, p.wait_ns));
             ++on;
-            if (!ok) break;
+            if (!ok) return;
             tm_fence_after();
         }
         // a list that is whole in this segment (and has nothing to be joined with) becomes outputs here; where
         // its units went to both warpgroups in turn, the second hands its record to the first
         const bool whole = p.n_own == 0 && s.v0 == 0 && s.v1 == s.per;
-        const bool joint = whole && !s.both && s.per > 1;
-        const long long slot = rows_slot(p, cta, s.item, s.v0 == 0);
+        const bool joint = whole && !s.both() && s.per > 1;
+        const long long item = s.item(p), slot = rows_slot(p, cta, item, s.v0 == 0);
         if (w == 1 && pending && (joint || !whole)) {   // the first warpgroup has read the record before it is written again
             ok = __all_sync(0xffffffffu, rows_wait(&B.read, rn & 1, B, p.wait_ns));
             ++rn;
-            if (!ok) break;
+            if (!ok) return;
             pending = false;
         }
         if (whole && !(joint && w == 1)) {
@@ -1121,24 +1196,24 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             if (joint) {
                 ok = __all_sync(0xffffffffu, rows_wait(&B.join, jn & 1, B, p.wait_ns));
                 ++jn;
-                if (!ok) break;
-                if (valid) {
+                if (!ok) return;
+                if (t.valid) {
                     const float m1 = __ldcg(other), l1 = __ldcg(other + 1), to = fmaxf(m, m1), base = to == -INFINITY ? 0.0f : to;
                     f = exp2f(m - base);
                     f1 = exp2f(m1 - base);
                     l = l * f + l1 * f1;
                 }
             }
-            if (any && mine) {
+            if (t.any && t.mine) {
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
                 f *= inv;
                 f1 *= inv;
-#pragma unroll 1
+#pragma unroll 2
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t o[16];
                     tm_ld16(tO + 16 * c, o);
                     tm_ready16(o);
-                    if (valid) {
+                    if (t.valid) {
                         float y[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * f;
@@ -1153,13 +1228,13 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                             }
                         }
                         if (p.out_dtype == DQK_BF16) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + at * D + 16 * c);
+                            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + t.at * D + 16 * c);
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
                                                     pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
                         } else {
-                            float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + at * D + 16 * c);
+                            float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.out) + t.at * D + 16 * c);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                         }
@@ -1169,28 +1244,22 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             }
             __syncwarp();
             if (joint && lane == 0) mbar_arrive(&B.read);
-        } else if (s.own || slot < p.rec_slots) {
-            float *rec = (s.own ? p.own_rec + rows_own_rec(cta + s.item, w, p.G, r) * rec_stride(D)
-                                : p.rec + rows_rec(slot, w, r) * rec_stride(D));
-            if (any) {
-                if (valid) {
-                    rec[0] = m;
-                    rec[1] = l;
-                }
-#pragma unroll 1
+        } else if (s.own(p) || slot < p.rec_slots) {
+            float *rec = (s.own(p) ? p.own_rec + rows_own_rec(cta + item, w, p.G, r) * rec_stride(D)
+                                   : p.rec + rows_rec(slot, w, r) * rec_stride(D));
+            if (t.valid) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);   // no unit of this segment: (-inf, 0) alone
+            if (t.any && t.mine) {
+#pragma unroll 2
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t o[16];
-                    if (mine) {
-                        tm_ld16(tO + 16 * c, o);
-                        tm_ready16(o);
-                    }
-                    if (valid) {
+                    tm_ld16(tO + 16 * c, o);
+                    tm_ready16(o);
+                    if (t.valid) {
                         float4 *dst = reinterpret_cast<float4 *>(rec + kRecHead + 16 * c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)   // no unit of this segment: an empty record
-                            dst[i] = mine ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
                     }
                     __syncwarp();
                 }
@@ -1203,9 +1272,12 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
         } else if (r == 0) {   // groups that overlap
             dqk_flag_error(kErrBounds);
         }
+        __syncwarp();
         tm_fence_before();   // the accumulator has been read before the next segment's first product
-        n += s.both ? 2 * units : units;
-        unit0 += units;
+        unit0 += s.units();
+        n += s.w * s.units();
+        s = sn;
+        t = tn;
     }
 }
 
@@ -1328,10 +1400,11 @@ struct RowsMerge {
             for (int e = 0; e < V; ++e) O[e] *= sc;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const float f = exp2f(m[k] - base);   // 0 for an empty record, whose o holds zeros
+                const float f = exp2f(m[k] - base);
+                const bool none = m[k] == -INFINITY && l[k] == 0.0f;   // an empty record: its o was not written
                 L = fmaf(f, l[k], L);
 #pragma unroll
-                for (int e = 0; e < V; ++e) O[e] = fmaf(f, o[k][e], O[e]);
+                for (int e = 0; e < V; ++e) O[e] = none ? O[e] : fmaf(f, o[k][e], O[e]);
             }
         }
     }
@@ -1429,8 +1502,8 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     const RowsCursor c = rows_cursor(p, b + 1, lane);
     if (c.u0 >= c.u1) return;
     const RowsList r = rows_list(p, c.list);
-    const int mt = c.k / p.hkv, j = c.k - mt * p.hkv, w = mt < r.tiles - 1 ? 2 : r.last;
-    const long long start = c.first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, q = rows_div(c.u0, b + 1);
+    const int mt = c.mt, j = c.j, w = mt < r.tiles - 1 ? 2 : r.last;
+    const long long start = c.start, q = rows_div(c.u0, b + 1);
     if (start >= c.u0 || rows_div(start, q) != b || start + (long long)(r.per - 1) * w < c.u0) return;
     const int first = rows_first(p, c.list), nr = min(kRowsTile, (rows_first(p, c.list + 1) - first) * p.G - mt * kRowsTile);
     for (int x = blockIdx.y * kRowsMergeRows + warp; x < min(nr, (int)(blockIdx.y + 1) * kRowsMergeRows); x += kRowsMergeWarps) {
