@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -11,8 +12,8 @@ LIB = os.path.join(HERE, "libdualqk.so")
 ROOT = os.path.dirname(HERE)
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v",
-              "--split-compile=0"]   # one translation unit: its kernels are optimised in parallel
+              "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
+UNITS = ["dualqk", "rows"]   # translation units, compiled side by side
 
 
 def sources() -> list[str]:
@@ -30,12 +31,18 @@ def stale() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or stale():
         nvcc = os.environ.get("NVCC", "nvcc")
-        cmd = [nvcc, *NVCC_FLAGS, "-o", LIB, os.path.join(CSRC, "dualqk.cu")]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or r.returncode:
-            print(r.stdout + r.stderr)
-        if r.returncode:
-            raise RuntimeError("nvcc failed building libdualqk.so")
+        with tempfile.TemporaryDirectory() as tmp:
+            objs = [os.path.join(tmp, u + ".o") for u in UNITS]
+            procs = [subprocess.Popen([nvcc, *NVCC_FLAGS, "-c", "-o", o, os.path.join(CSRC, u + ".cu")],
+                                      stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                     for u, o in zip(UNITS, objs)]
+            logs = [p.communicate()[0] for p in procs]
+            link = subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", LIB, *objs], capture_output=True, text=True) \
+                if not any(p.returncode for p in procs) else None
+            if verbose or link is None or link.returncode:
+                print("".join(logs) + (link.stdout + link.stderr if link else ""))
+            if link is None or link.returncode:
+                raise RuntimeError("nvcc failed building libdualqk.so")
     return LIB
 
 

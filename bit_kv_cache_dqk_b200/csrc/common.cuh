@@ -130,8 +130,7 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_floa
 
 }  // namespace dqk
 
-// One error word per device, OR-ed by kernels, read by dqk_last_device_error.
-// (libdualqk is a single translation unit: dualqk.cu includes every kernel.)
-__device__ unsigned int g_dqk_device_error = 0;
+// One error word per device and translation unit, OR-ed by kernels, read by dqk_last_device_error.
+static __device__ unsigned int g_dqk_device_error = 0;
 
 __device__ __forceinline__ void dqk_flag_error(unsigned bits) { atomicOr(&g_dqk_device_error, bits); }

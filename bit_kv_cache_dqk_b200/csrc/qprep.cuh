@@ -188,8 +188,8 @@ __device__ __forceinline__ void select_kept(const float *qp, int nk, int lane, u
 // The rare paths of the piece arithmetic (subnormal operands), kept out of
 // line: the prologue runs once per launch, so its code is fetched cold and
 // every inlined instruction costs.
-__device__ __noinline__ float ldexp_rare(float x, int e) { return ldexpf(x, e); }
-__device__ __noinline__ int exp_offset_rare(float sh, float tg) {
+static __device__ __noinline__ float ldexp_rare(float x, int e) { return ldexpf(x, e); }
+static __device__ __noinline__ int exp_offset_rare(float sh, float tg) {
     int e = ilogbf(sh) - ilogbf(tg);
     if (ldexpf(sh, -e) < tg) --e;
     return e;

@@ -47,6 +47,7 @@ constexpr int kRowsTile = 256;                    // row heads of an item
 constexpr int kRowsHalf = 128;                    // row heads of a job
 constexpr int kRowsKv = 128;                      // tokens of a unit
 constexpr int kRowsPages = kRowsKv / kPage;       // pages of a unit
+constexpr int kRowsMaxCtas = 160;
 constexpr int kRowsUnpackWarps = 4;
 constexpr int kRowsFlags = 8;                     // units in flight at most (page flags)
 // fp16 weights (INT2) are carried times 2^6, and so is their sum (the factor leaves with it): a
@@ -72,7 +73,9 @@ struct RowsParams {
     const void *q;
     const float *q_scale;
     float qs;
+    struct RowsPlan *plan;      // what the merge needs of the split (written by the row kernel)
     float *rec, *own_rec;       // split records of the groups' and of the own items
+    bool slot_pairs;            // see rows_slot
     long long rec_slots;        // slots `rec` holds (row_start out of order could ask for more)
     void *out;
     int out_dtype;
@@ -271,12 +274,43 @@ struct RowsWalk {
     }
 };
 
+// What the row kernel leaves for the merge: weighted units per CTA, where each CTA's walk starts (without own
+// lists), or each list's first weighted unit and the row tiles before it (with).
+struct RowsPlan {
+    long long q;
+    RowsCursor cursor[kRowsMaxCtas];
+    struct {
+        long long first, tile0;
+    } list[1];   // n_groups + n_own of them
+};
+__host__ __device__ constexpr size_t rows_plan_bytes(size_t lists) { return sizeof(RowsPlan) + 16 * lists; }
+
+// By one warp of the grid's first CTA.
+__device__ __forceinline__ void rows_write_plan(const RowsParams &p, int lane) {
+    const int n = p.n_groups + p.n_own;
+    long long base = 0, tbase = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        RowsList r{0, 1, 0, 0};
+        if (i < n) r = rows_list(p, i);
+        const int t = i < p.n_groups ? r.tiles : 0;
+        const long long ui = warp_scan(r.units, lane), ti = warp_scan(t, lane);
+        if (i < n) {
+            p.plan->list[i].first = base + ui - r.units;
+            p.plan->list[i].tile0 = tbase + ti - t;
+        }
+        base += __shfl_sync(0xffffffffu, ui, 31);
+        tbase += __shfl_sync(0xffffffffu, ti, 31);
+    }
+    if (lane == 0) p.plan->q = rows_share(base, p.num_ctas);
+}
+
 // Record slots of the groups' items.  With own lists every segment is joined with another:
 // slot CTA + item (a CTA's segments are of consecutive items).  Without, only items that cross
-// a CTA's border are: slot 2 CTA for the part of an item that began in an earlier CTA, 2 CTA + 1
-// for one that begins here.
+// a CTA's border are: the same, or, where there are more items than CTAs (slot_pairs), slot 2 CTA
+// for the part of an item that began in an earlier CTA, 2 CTA + 1 for one that begins here.
 __device__ __forceinline__ long long rows_slot(const RowsParams &p, long long cta, long long item, bool begins) {
-    return p.n_own ? cta + item : 2 * cta + (begins ? 1 : 0);
+    return p.slot_pairs ? 2 * cta + (begins ? 1 : 0) : cta + item;
 }
 // Record row: warpgroup g's row r of a slot.
 __device__ __forceinline__ size_t rows_rec(long long slot, int g, int r) { return ((size_t)slot * 2 + g) * kRowsHalf + r; }
@@ -443,23 +477,30 @@ struct PageInt2 {
             }
         }
     }
-    __device__ __forceinline__ void load(uint32_t blk, int lane) {
-        constexpr Layout L = make_layout(D, VCH0 ? 1 : 0, NS);
+    static constexpr Layout kL = make_layout(D, VCH0 ? 1 : 0, NS);
+    __device__ __forceinline__ void load_keys(uint32_t blk, int lane) {
         gid = lane >> 2;
         tig = lane & 3;
-        words<NG>(kw, blk + L.kc + lane * 4 * NG);
-        words<NG>(vw, blk + L.vc + lane * 4 * NG);
-        const uint32_t k0w = ld_s32(blk + L.k0 + gid * 4);
+        words<NG>(kw, blk + kL.kc + lane * 4 * NG);
+        const uint32_t k0w = ld_s32(blk + kL.k0 + gid * 4);
         k0[0] = bf16_to_f16_sat(k0w & 0xffffu);
         k0[1] = bf16_to_f16_sat(k0w >> 16);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            pairs(ks[h], blk + L.ks + (gid + 8 * h) * 2 * NS);
-            pairs(km[h], blk + L.km + (gid + 8 * h) * 2 * NS);
-            words<NS>(vs[h], blk + L.vs + (tig + 4 * h) * 4 * NS);
-            words<NS>(vm[h], blk + L.vm + (tig + 4 * h) * 4 * NS);
+            pairs(ks[h], blk + kL.ks + (gid + 8 * h) * 2 * NS);
+            pairs(km[h], blk + kL.km + (gid + 8 * h) * 2 * NS);
+        }
+    }
+    __device__ __forceinline__ void load_values(uint32_t blk, int lane) {
+        gid = lane >> 2;
+        tig = lane & 3;
+        words<NG>(vw, blk + kL.vc + lane * 4 * NG);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            words<NS>(vs[h], blk + kL.vs + (tig + 4 * h) * 4 * NS);
+            words<NS>(vm[h], blk + kL.vm + (tig + 4 * h) * 4 * NS);
             if constexpr (VCH0) {
-                const uint32_t w = ld_s32(blk + L.v0 + (tig + 4 * h) * 4);
+                const uint32_t w = ld_s32(blk + kL.v0 + (tig + 4 * h) * 4);
                 v0[h] = (uint32_t)bf16_to_f16_sat(w & 0xffffu) | ((uint32_t)bf16_to_f16_sat(w >> 16) << 16);
             }
         }
@@ -699,6 +740,8 @@ __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtenso
 
 // INT2: packed blocks -> fp16 operand tiles.  Keys as rows of tokens; values as
 // rows of channels (the order their codes are stored in), 64 tokens per 128-byte row.
+// A unit's keys come first, and on their own: their tile is free as soon as the scores of
+// two units before are formed, the values' only after that unit's weights.
 template <int D, int NS, bool VCH0>
 __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *raw, int warp,
                                             int lane) {
@@ -708,41 +751,47 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
     int unit = 0;
     bool ok = true;
     const int mi = lane >> 3, r8 = lane & 7, tig = lane & 3;
+    // rows of the matrix this lane addresses: keys, token 8 (mi >> 1) + r8 of the page, column chunk
+    // 2s + (mi & 1); values, channel 16m + 8 (mi >> 1) + r8, the page's tokens of half mi & 1
+    const uint32_t tile0 = smem_addr(tiles), ka = (uint32_t)(64 * (mi >> 1) + r8) * 128,
+                   va = (uint32_t)(mi & 1) * (D * 128) + (uint32_t)(8 * (mi >> 1) + r8) * 128;
     for (s.begin(p, B.cursor); ok && s.live; s.next(p)) {
         for (int v = s.v0; ok && v < s.v1; ++v, ++unit) {
-            const int rs = rr.st;
-            ok = rows_wait(&B.raw_full[rs], rr.phase, B, p.wait_ns);
-            rr.next(p.raw_stages);
-            const int sk = rk.st, sv = p.ktiles + rv.st;
-            ok = ok && rows_wait(&B.empty[sk], rk.phase ^ 1u, B, p.wait_ns);
-            ok = ok && rows_wait(&B.empty[sv], rv.phase ^ 1u, B, p.wait_ns);
-            rk.next(p.ktiles);
-            rv.next(p.vtiles);
+            const int rs = rr.st, sk = rk.st, sv = p.ktiles + rv.st, nv = s.len - v * kRowsKv, pages = 2 * rows_pairs(nv);
+            ok = rows_wait(&B.raw_full[rs], rr.phase, B, p.wait_ns) && rows_wait(&B.empty[sk], rk.phase ^ 1u, B, p.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
-            const uint32_t kt = smem_addr(tiles) + (uint32_t)sk * kTile, vt = smem_addr(tiles) + (uint32_t)sv * kTile;
+            const uint32_t blk = smem_addr(raw) + (uint32_t)(rs * kRowsPages * p.bb);
 #pragma unroll 1
-            for (int pg = warp; pg < 2 * rows_pairs(s.len - v * kRowsKv); pg += kRowsUnpackWarps) {
-                // rows of the matrix this lane addresses: keys, token 8 (mi >> 1) + r8 of the page, column chunk
-                // 2s + (mi & 1); values, channel 16m + 8 (mi >> 1) + r8, the page's tokens of half mi & 1
-                const uint32_t ka = kt + (uint32_t)(64 * (mi >> 1) + 8 * pg + r8) * 128;
-                const uint32_t va = vt + (uint32_t)(mi & 1) * (D * 128) + (uint32_t)(8 * (mi >> 1) + r8) * 128 +
-                                    (uint32_t)((pg ^ r8) << 4);
+            for (int pg = warp; pg < pages; pg += kRowsUnpackWarps) {
+                if (!((have >> pg) & 1u)) continue;   // its scores are masked
+                PageInt2<D, NS, VCH0> b;
+                b.load_keys(blk + (uint32_t)(pg * p.bb), lane);
+                const uint32_t row = tile0 + (uint32_t)sk * kTile + ka + (uint32_t)pg * 1024;
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st) {
+                    uint32_t k4[4];
+                    b.keys(st, k4);
+                    const int c = 2 * st + (mi & 1);
+                    stmatrix_x4(row + (uint32_t)(c >> 3) * (kRowsKv * 128) + (uint32_t)(((c & 7) ^ r8) << 4), k4);
+                }
+            }
+            fence_proxy_async_shared();   // the tiles are read by the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.full[sk]);
+            ok = __all_sync(0xffffffffu, rows_wait(&B.empty[sv], rv.phase ^ 1u, B, p.wait_ns));
+            if (!ok) break;
+#pragma unroll 1
+            for (int pg = warp; pg < pages; pg += kRowsUnpackWarps) {
+                const uint32_t row = tile0 + (uint32_t)sv * kTile + va + (uint32_t)((pg ^ r8) << 4);
                 if ((have >> pg) & 1u) {
                     PageInt2<D, NS, VCH0> b;
-                    b.load(smem_addr(raw) + (uint32_t)((rs * kRowsPages + pg) * p.bb), lane);
-#pragma unroll
-                    for (int st = 0; st < D / 16; ++st) {
-                        uint32_t k4[4];
-                        b.keys(st, k4);
-                        const int c = 2 * st + (mi & 1);
-                        stmatrix_x4(ka + (uint32_t)(c >> 3) * (kRowsKv * 128) + (uint32_t)(((c & 7) ^ r8) << 4), k4);
-                    }
+                    b.load_values(blk + (uint32_t)(pg * p.bb), lane);
                     // tokens past the list's end hold stale bytes: zeros, so that they add nothing
-                    const int nv = s.len - (v * kRowsPages + pg) * kPage;
-                    const uint32_t lo = (2 * tig < nv ? 0x0000ffffu : 0u) | (2 * tig + 1 < nv ? 0xffff0000u : 0u);
-                    const uint32_t hi = (2 * tig + 8 < nv ? 0x0000ffffu : 0u) | (2 * tig + 9 < nv ? 0xffff0000u : 0u);
+                    const int n = nv - kPage * pg;
+                    const uint32_t lo = (2 * tig < n ? 0x0000ffffu : 0u) | (2 * tig + 1 < n ? 0xffff0000u : 0u);
+                    const uint32_t hi = (2 * tig + 8 < n ? 0x0000ffffu : 0u) | (2 * tig + 9 < n ? 0xffff0000u : 0u);
 #pragma unroll
                     for (int m = 0; m < D / 16; ++m) {
                         uint32_t v4[4];
@@ -751,21 +800,23 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
                         v4[1] &= hi;
                         v4[2] &= lo;
                         v4[3] &= hi;
-                        stmatrix_x4(va + (uint32_t)(m * 16 * 128), v4);
+                        stmatrix_x4(row + (uint32_t)(m * 16 * 128), v4);
                     }
                 } else {
                     const uint32_t z[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                    for (int m = 0; m < D / 16; ++m) stmatrix_x4(va + (uint32_t)(m * 16 * 128), z);
+                    for (int m = 0; m < D / 16; ++m) stmatrix_x4(row + (uint32_t)(m * 16 * 128), z);
                 }
             }
-            fence_proxy_async_shared();   // the tiles are read by the tensor core
+            fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&B.full[sk]);
                 mbar_arrive(&B.full[sv]);
                 mbar_arrive(&B.raw_empty[rs]);
             }
+            rr.next(p.raw_stages);
+            rk.next(p.ktiles);
+            rv.next(p.vtiles);
         }
     }
     // the last arrivals on `empty` come before the block leaves
@@ -958,18 +1009,19 @@ __device__ __forceinline__ void rows_mask(uint32_t tS, int nv, uint32_t have, in
 template <bool F16>
 __device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2, float2 b2, uint32_t *pk, float2 &s0, float2 &s1,
                                              float &m0, float &m1) {
+    float2 e[8], y[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        const float2 a = make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
-        const float2 b = make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
-        m0 = max3(m0, a.x, a.y);
-        m1 = max3(m1, b.x, b.y);
-        const float2 ea = fma2(a, q2, b2), eb = fma2(b, q2, b2);
-        const float2 pa = make_float2(fast_exp2(ea.x), fast_exp2(ea.y)), pb = make_float2(fast_exp2(eb.x), fast_exp2(eb.y));
-        s0 = add2(s0, pa);
-        s1 = add2(s1, pb);
-        pk[i / 2] = F16 ? pack_f16x2(pa.x, pa.y) : pack_bf16x2(pa.x, pa.y);
-        pk[i / 2 + 1] = F16 ? pack_f16x2(pb.x, pb.y) : pack_bf16x2(pb.x, pb.y);
+    for (int i = 0; i < 8; ++i) e[i] = fma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), q2, b2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = make_float2(fast_exp2(e[i].x), fast_exp2(e[i].y));
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        m0 = max3(m0, __uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        m1 = max3(m1, __uint_as_float(u[2 * i + 2]), __uint_as_float(u[2 * i + 3]));
+        s0 = add2(s0, y[i]);
+        s1 = add2(s1, y[i + 1]);
+        pk[i] = F16 ? pack_f16x2(y[i].x, y[i].y) : pack_bf16x2(y[i].x, y[i].y);
+        pk[i + 1] = F16 ? pack_f16x2(y[i + 1].x, y[i + 1].y) : pack_bf16x2(y[i + 1].x, y[i + 1].y);
     }
 }
 
@@ -1009,7 +1061,7 @@ __device__ __forceinline__ float rows_largest(uint32_t tS, float qs) {
 // whose scores pass the reference by more than the slack (rare) is taken again after the reference
 // has moved and what was summed -- l, and the accumulator, once `settled` has waited for it -- has been rescaled.
 template <int D, bool F16, typename Settled>
-__device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, float qs, float lift, float &m, float &l,
+__device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, float lift, float &m, float &l,
                                           Settled settled) {
     uint32_t pk[32];
     const float2 q2 = make_float2(qs, qs);
@@ -1028,7 +1080,7 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, float qs, fl
         for (int c = 0; c < kAtOnce; ++c) rows_weights<F16>(x[c], q2, b2, pk + 8 * (c0 + c), s0, s1, m0, m1);
     }
     const float mx = fmaxf(m0, m1) * qs;
-    const bool move = mx > m + kRowsSlack;
+    const bool move = valid && mx > m + kRowsSlack;   // (lanes without a row hold anything)
     if (__any_sync(0xffffffffu, move)) {
         // the references are whole numbers: moving one scales by a power of two
         const float to = move ? ceilf(mx) : m, f = !move || m == -INFINITY ? 1.0f : fast_exp2(m - to);
@@ -1157,7 +1209,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     if (none) m = ceilf(rows_largest(tS, qs));   // no reference yet
                     // the half before this one may still be on its way into the accumulator (the one before that is not:
                     // these scores lie where its weights were)
-                    ok = rows_half<D, kFmt == 2>(tS + 64 * h, tO, qs, T::kLift, m, l, [&]() {
+                    ok = rows_half<D, kFmt == 2>(tS + 64 * h, tO, t.valid, qs, T::kLift, m, l, [&]() {
                         if (none) return 0;
                         if (!__all_sync(0xffffffffu, rows_wait(&B.o_step[w], (pn - 1) & 1u, B, p.wait_ns))) return -1;
                         tm_fence_after();
@@ -1319,8 +1371,12 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     }
     if (warp == 8) {
         const RowsCursor c = rows_cursor(p, blockIdx.x, lane);
-        if (lane == 0) B.cursor = c;
+        if (lane == 0) {
+            B.cursor = c;
+            if (p.n_own == 0) p.plan->cursor[blockIdx.x] = c;
+        }
     }
+    if (warp == 10 && blockIdx.x == 0) rows_write_plan(p, lane);
     if (warp == 9) tm_alloc(&B.tmem, 512);
     tm_fence_before();
     __syncthreads();
@@ -1352,7 +1408,7 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsMerge {
-    static constexpr int V = D / 32, kBatch = 8;
+    static constexpr int V = D / 32, kBatch = 4;
     float M = -INFINITY, L = 0.0f, O[V] = {};
     // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose weighted units start
     // at `start`: CTAs cf .. cl, both warpgroups' where the units went to one and the other.
@@ -1426,92 +1482,63 @@ struct RowsMerge {
     }
 };
 
-constexpr int kRowsMergeWarps = 8, kRowsMergeHeads = 16, kRowsMergeRows = 32;
+constexpr int kRowsMergeWarps = 8;
 
-// With own lists (decode): CTA = (query row, up to 16 of its heads), a warp per head, over the records of its
-// group's item and its own.
+// With own lists (decode): a warp per row head, over the records of its group's item and its own.
 template <int D>
-__global__ void __launch_bounds__(32 * kRowsMergeHeads) k_rows_merge(const __grid_constant__ RowsParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int row = blockIdx.x, h = blockIdx.y * warps + warp;
-    __shared__ long long sh_q, sh_before, sh_tile0, sh_own;
-    __shared__ int sh_group;
-    grid_dependency_wait();
-    if (warp == 0) {
-        long long U, tiles;
-        rows_sums(p, p.n_groups + p.n_own, lane, U, tiles);
-        if (lane == 0) sh_q = rows_share(U, p.num_ctas);
-    }
-    if (warp == 1 % warps) {
-        int g = -1;
-        long long before = 0, tile0 = 0;
-        for (int i0 = 0; i0 < p.n_groups; i0 += 32) {
-            const int i = i0 + lane;
-            const unsigned hit =
-                __ballot_sync(0xffffffffu, i < p.n_groups && rows_first(p, i) <= row && row < rows_first(p, i + 1));
-            if (hit) {
-                g = i0 + __ffs(hit) - 1;
-                break;
-            }
-        }
-        if (g >= 0) rows_sums(p, g, lane, before, tile0);
-        if (lane == 0) {
-            sh_group = g;
-            sh_before = before;
-            sh_tile0 = tile0;
-        }
-    }
-    if (warp == 2 % warps) {
-        long long before, tiles;
-        rows_sums(p, p.n_groups + row, lane, before, tiles);
-        if (lane == 0) sh_own = before;
-    }
-    __syncthreads();
+__global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __grid_constant__ RowsParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x, h = blockIdx.y * kRowsMergeWarps + warp;
     if (h >= p.hq) return;
-    const int j = h / p.G, hh = h - j * p.G, g = sh_group;
-    const long long q = sh_q;
+    const int j = h / p.G, hh = h - j * p.G;
+    grid_dependency_wait();
+    const long long q = p.plan->q, own_first = p.plan->list[p.n_groups + row].first;
+    const int per = rows_list(p, p.n_groups + row).per;
+    int g = -1;   // the group of the row
+    for (int i0 = 0; i0 < p.n_groups && g < 0; i0 += 32) {
+        const int i = i0 + lane;
+        const unsigned hit =
+            __ballot_sync(0xffffffffu, i < p.n_groups && rows_first(p, i) <= row && row < rows_first(p, i + 1));
+        if (hit) g = i0 + __ffs(hit) - 1;
+    }
     RowsMerge<D> acc;
     if (g >= 0) {
         const RowsList r = rows_list(p, g);
+        const long long first = p.plan->list[g].first, tile0 = p.plan->list[g].tile0;
         const int rr = (row - rows_first(p, g)) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? 2 : r.last;
-        acc.take(p, false, sh_before + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, r.per, w == 2, q,
-                 (sh_tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
+        acc.take(p, false, first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, r.per, w == 2, q,
+                 (tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
     }
-    const int per = rows_list(p, p.n_groups + row).per;
-    acc.take(p, true, sh_own + (long long)j * per, per, 0, q, (long long)row * p.hkv + j, hh, lane);
+    acc.take(p, true, own_first + (long long)j * per, per, 0, q, (long long)row * p.hkv + j, hh, lane);
     acc.store(p, (size_t)row * p.hq + h, lane);
 }
 
-// Without own lists, CTA (b, y): row heads 32 y .. 32 y + 31 of the item that begins in CTA b of the row kernel and
-// goes on in the next one (every other item's outputs are written already); the CTAs behind those zero the rows of
-// groups without any token.
+// Without own lists, CTA (b, y): row heads 8 y .. 8 y + 7 of the item that begins in CTA b of the row kernel and
+// goes on in the next one (every other item's outputs are written already), a warp each; the CTAs behind those zero
+// the rows of groups without any token.
 template <int D>
 __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const __grid_constant__ RowsParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, x = blockIdx.y * kRowsMergeWarps + warp;
     grid_dependency_wait();
     if (b >= p.num_ctas - 1) {
         for (int g = b - (p.num_ctas - 1); g < p.n_groups; g += (int)gridDim.x - (p.num_ctas - 1)) {
             if (rows_list(p, g).per > 0) continue;
-            const size_t at = (size_t)rows_first(p, g) * p.hq * D, n = (size_t)max(rows_first(p, g + 1) - rows_first(p, g), 0) * p.hq * D;
+            const size_t at = (size_t)rows_first(p, g) * p.hq, n = (size_t)max(rows_first(p, g + 1) - rows_first(p, g), 0) * p.hq;
             const RowsMerge<D> zero;
-            for (size_t x = (size_t)blockIdx.y * kRowsMergeWarps + warp; x < n / D; x += (size_t)gridDim.y * kRowsMergeWarps)
-                zero.store(p, at / D + x, lane);
+            for (size_t i = x; i < n; i += (size_t)gridDim.y * kRowsMergeWarps) zero.store(p, at + i, lane);
         }
         return;
     }
-    const RowsCursor c = rows_cursor(p, b + 1, lane);
-    if (c.u0 >= c.u1) return;
+    const RowsCursor c = p.plan->cursor[b + 1];
+    const long long q = p.plan->q;
+    if (c.u0 >= c.u1 || c.start >= c.u0) return;
     const RowsList r = rows_list(p, c.list);
-    const int mt = c.mt, j = c.j, w = mt < r.tiles - 1 ? 2 : r.last;
-    const long long start = c.start, q = rows_div(c.u0, b + 1);
-    if (start >= c.u0 || rows_div(start, q) != b || start + (long long)(r.per - 1) * w < c.u0) return;
-    const int first = rows_first(p, c.list), nr = min(kRowsTile, (rows_first(p, c.list + 1) - first) * p.G - mt * kRowsTile);
-    for (int x = blockIdx.y * kRowsMergeRows + warp; x < min(nr, (int)(blockIdx.y + 1) * kRowsMergeRows); x += kRowsMergeWarps) {
-        const int rr = mt * kRowsTile + x;
-        RowsMerge<D> acc;
-        acc.take(p, false, start, r.per, w == 2, q, 0, x, lane);
-        acc.store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)j * p.G + rr % p.G, lane);
-    }
+    const int first = rows_first(p, c.list), heads = (rows_first(p, c.list + 1) - first) * p.G;
+    const int w = c.mt < r.tiles - 1 ? 2 : r.last, rr = c.mt * kRowsTile + x;
+    if (x >= kRowsTile || rr >= heads || c.start < b * q || c.start + (long long)(r.per - 1) * w < c.u0) return;
+    RowsMerge<D> acc;
+    acc.take(p, false, c.start, r.per, w == 2, q, (c.tile0 + c.mt) * p.hkv + c.j, x, lane);
+    acc.store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)c.j * p.G + rr % p.G, lane);
 }
 
 }  // namespace dqk
