@@ -388,6 +388,7 @@ dqk_status run_rows(const RowsCall &a) {
     p.hq = L->num_q_heads;
     p.hkv = L->num_kv_heads;
     p.G = P.G;
+    p.head = a.int2 ? kRowsHeadInt2 : kRowsHeadBf16;
     p.bb = P.bb;
     p.num_ctas = (int)std::max<long long>(1, std::min<long long>(std::min(sms, kRowsMaxCtas), P.max_units));
     p.wait_ns = kRingWaitNs;

@@ -13,7 +13,7 @@
 // Work split: item = (group, tile of 256 row heads, kv head), then (own list,
 // kv head); unit = 128 tokens of an item.  A unit of a tile of more than 128
 // row heads weighs 2, others 1; CTA c takes the units that start in
-// [cq, (c+1)q) of all U weighted units, q = ceil(U / C), so every CTA does
+// [cq, (c+1)q) of the cost U of all units, q = ceil(U / C), so every CTA does
 // about the same work whatever the lengths.
 //
 // One CTA per SM, warp-specialized around the tensor core (tcgen05, operands in
@@ -79,6 +79,7 @@ struct RowsParams {
     long long rec_slots;        // slots `rec` holds (row_start out of order could ask for more)
     void *out;
     int out_dtype;
+    int head;                   // cost of an item besides its units
     int hq, hkv, G, bb, ktiles, vtiles, raw_stages, num_ctas;
     unsigned long long wait_ns;
 };
@@ -96,24 +97,35 @@ __device__ __forceinline__ int rows_first(const RowsParams &p, int g) {
     return min(max(p.row_start[g], 0), p.total_rows);
 }
 
-// A list's shape: row tiles (the last one's weight), units of a tile, weighted units in all.
+// The work is split by cost: of a unit that both warpgroups take, of one that goes to one of them, and of
+// an item besides (p.head: its queries, its outputs, the pipeline's end and start).  A CTA's clocks, head_dim
+// 128: BF16 4300, 2630 and 4600; INT2 5240, 3500 and 2800; but units of one list beside others' are
+// slower, and the ratios are those that measured best (us; cross attention of 4 x 1024 queries over 4096 states, two
+// documents of 32K tokens, INT2 document of 128K): 2 : 1 : 0 312, 96, 359; 3 : 2 : 3 or 2 247, 83, 282;
+// 5 : 4 : 6 or 4 218, 82, 285; 5 : 4 : 9 or 6 218, 82, 286 and less for short lists; 9 : 8 : 12 or 8 217, 83, 288.
+constexpr int kRowsBothCost = 5, kRowsOneCost = 4, kRowsHeadBf16 = 9, kRowsHeadInt2 = 6;
+
+// A list's shape: row tiles (the cost of a unit of the last one), units of a tile, their cost in all.
 struct RowsList {
     int tiles, last, per;
     long long units;
 };
+// Cost of an item of `per` units.
+__device__ __forceinline__ long long rows_cost(const RowsParams &p, int per, int w) { return p.head + (long long)per * w; }
 __device__ __forceinline__ RowsList rows_list(const RowsParams &p, int i) {
     RowsList r;
     if (i < p.n_groups) {
         const int n = max(rows_first(p, i + 1) - rows_first(p, i), 0) * p.G;
         r.tiles = (n + kRowsTile - 1) / kRowsTile;
-        r.last = n - (r.tiles - 1) * kRowsTile > kRowsHalf ? 2 : 1;
+        r.last = n - (r.tiles - 1) * kRowsTile > kRowsHalf ? kRowsBothCost : kRowsOneCost;
         r.per = rows_units(rows_len(p.kv_lens, i, p.max_pages));
     } else {
         r.tiles = 1;
-        r.last = 1;
+        r.last = kRowsOneCost;
         r.per = rows_units(rows_len(p.own_lens, i - p.n_groups, p.own_max_pages));
     }
-    r.units = r.tiles ? (long long)p.hkv * r.per * (2 * (r.tiles - 1) + r.last) : 0;
+    r.units = r.tiles && r.per ? (long long)p.hkv * ((r.tiles - 1) * rows_cost(p, r.per, kRowsBothCost) + rows_cost(p, r.per, r.last))
+                               : 0;
     return r;
 }
 
@@ -127,7 +139,7 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
     return x;
 }
 
-// Weighted units and row tiles of the lists before list n; warp-collective.
+// Cost and row tiles of the lists before list n; warp-collective.
 __device__ __forceinline__ void rows_sums(const RowsParams &p, int n, int lane, long long &units, long long &tiles) {
     long long u = 0, t = 0;
     for (int i = lane; i < n; i += 32) {
@@ -144,18 +156,18 @@ __device__ __forceinline__ void rows_sums(const RowsParams &p, int n, int lane, 
     tiles = t;
 }
 
-// The start of a CTA's walk: its weighted units [u0, u1), the item that holds u0 (first weighted
-// unit `start`), and the row tiles of the groups before its list.
+// The start of a CTA's walk: its range of cost [u0, u1) -- a unit is its own if it begins there --, the item
+// that holds u0 (whose first unit begins at `start`), and the row tiles of the groups before its list.
 struct RowsCursor {
     long long u0, u1, start, tile0;
     int list, mt, j;
 };
 
-// Weighted units per CTA (and the general quotient: 32-bit division where it fits).
+// Cost per CTA (and the general quotient: 32-bit division where it fits).
 __device__ __forceinline__ long long rows_div(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
-__device__ __forceinline__ long long rows_share(long long U, int ctas) { return max(rows_div(U + ctas - 1, ctas), 1LL); }
+__device__ __forceinline__ long long rows_share(long long U, int ctas) { return max(rows_div(U + ctas - 1, ctas), (long long)kRowsOneCost); }
 
 // The CTA's cursor at its first list; warp-collective.
 __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, int lane) {
@@ -183,12 +195,13 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
             int mt = 0, j = 0;   // the (tile, kv head) that holds u0
             long long start = 0;
             if (hit) {
-                const long long first = base + ui - r.units, local = c.u0 - first, full = (long long)(r.tiles - 1) * p.hkv * r.per * 2;
-                const int w = local < full ? 2 : r.last;
-                const int k = (int)rows_div(local < full ? local : local - full, (long long)w * r.per);
+                const long long first = base + ui - r.units, local = c.u0 - first, both = rows_cost(p, r.per, kRowsBothCost),
+                                full = (long long)(r.tiles - 1) * p.hkv * both;
+                const long long cost = local < full ? both : rows_cost(p, r.per, r.last);
+                const int k = (int)rows_div(local < full ? local : local - full, cost);
                 mt = local < full ? k / p.hkv : r.tiles - 1;
                 j = local < full ? k - mt * p.hkv : k;
-                start = first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w;
+                start = first + (long long)mt * p.hkv * both + (long long)j * cost + p.head;
             }
             const int src = __ffs(m) - 1;
             c.list = i0 + src;
@@ -204,13 +217,17 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
     return c;
 }
 
-__device__ __forceinline__ long long ceil_half(long long x, int w) { return w == 2 ? (x + 1) >> 1 : x; }
+// Units of cost w, one after another, that begin before x.
+__device__ __forceinline__ int rows_begun(long long x, int w, int per) {
+    const unsigned all = (unsigned)(per * w), y = x <= 0 ? 0u : x >= all ? all : (unsigned)x;
+    return (int)(w == kRowsOneCost ? (y + kRowsOneCost - 1) / kRowsOneCost : (y + kRowsBothCost - 1) / kRowsBothCost);
+}
 
 // Walks the segments -- stretches [v0, v1) of one item's units -- of a CTA in order.
 struct RowsWalk {
-    long long start, u1, tile0;     // the item's first weighted unit, the CTA's end, row tiles of the groups before
+    long long start, u1, tile0;     // where the item's first unit begins, the CTA's end, row tiles of the groups before
     int list, tiles, last, per, len, row0, heads;   // the list: shape, tokens, first query row, row heads
-    int mt, j, w;                   // the item: row tile, kv head, weight
+    int mt, j, w;                   // the item: row tile, kv head, cost of a unit
     int v0, v1;
     bool live;
     __device__ __forceinline__ void load(const RowsParams &p) {
@@ -238,13 +255,13 @@ struct RowsWalk {
         tile0 = c.tile0;
         mt = c.mt;
         j = c.j;
-        w = mt < tiles - 1 ? 2 : last;
-        v0 = (int)ceil_half(c.u0 - start, w);
-        v1 = (int)ceil_half(min(u1 - start, (long long)per * w), w);
-        if (v0 >= v1) next(p);   // the CTA's only unit of it starts one earlier
+        w = mt < tiles - 1 ? kRowsBothCost : last;
+        v0 = rows_begun(c.u0 - start, w, per);
+        v1 = rows_begun(u1 - start, w, per);
+        if (v0 >= v1) next(p);   // none of its units begins in the CTA's range
     }
     __device__ __forceinline__ void next(const RowsParams &p) {
-        start += (long long)per * w;
+        start += rows_cost(p, per, w);
         if (++j == p.hkv) {
             j = 0;
             if (++mt == tiles) {
@@ -258,15 +275,16 @@ struct RowsWalk {
                 } while (tiles == 0 || per == 0);
                 mt = 0;
             }
-            w = mt < tiles - 1 ? 2 : last;
+            w = mt < tiles - 1 ? kRowsBothCost : last;
         }
-        live = start < u1;
         v0 = 0;
-        v1 = live ? (int)ceil_half(min(u1 - start, (long long)per * w), w) : 0;
+        v1 = rows_begun(u1 - start, w, per);
+        live = v1 > 0;
     }
     __device__ __forceinline__ bool own(const RowsParams &p) const { return list >= p.n_groups; }
-    __device__ __forceinline__ bool both() const { return w == 2; }   // both warpgroups take every unit
+    __device__ __forceinline__ bool both() const { return w == kRowsBothCost; }   // both warpgroups take every unit
     __device__ __forceinline__ int units() const { return v1 - v0; }
+    __device__ __forceinline__ int jobs() const { return both() ? 2 * units() : units(); }
     __device__ __forceinline__ int rows() const { return min(kRowsTile, heads - mt * kRowsTile); }
     // record slot: CTA + item
     __device__ __forceinline__ long long item(const RowsParams &p) const {
@@ -274,8 +292,8 @@ struct RowsWalk {
     }
 };
 
-// What the row kernel leaves for the merge: weighted units per CTA, where each CTA's walk starts (without own
-// lists), or each list's first weighted unit and the row tiles before it (with).
+// What the row kernel leaves for the merge: cost per CTA, where each CTA's walk starts (without own
+// lists), or where each list's cost begins and the row tiles before it (with).
 struct RowsPlan {
     long long q;
     RowsCursor cursor[kRowsMaxCtas];
@@ -637,7 +655,7 @@ struct RowsUnits {
     __device__ __forceinline__ bool first() const { return s.both() ? v == s.v0 : v < s.v0 + 2; }
     __device__ __forceinline__ bool last() const { return s.both() ? v == s.v1 - 1 : v >= s.v1 - 2; }
     __device__ __forceinline__ void next(const RowsParams &p) {
-        n += s.w;
+        n += s.both() ? 2 : 1;
         ++unit;
         k.next(p.ktiles);
         t.next(p.vtiles);
@@ -1184,7 +1202,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
         if (!t.mine) {
             sn = s;
             sn.next(p);
-            tn = rows_part(p, sn, n + s.w * s.units(), w, r);
+            tn = rows_part(p, sn, n + s.jobs(), w, r);
             rows_query<D, kFmt>(p, tn, qtile, r);
         }
         for (int v = t.vf; v < s.v1; v += step) {
@@ -1199,7 +1217,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     // in while these scores become weights
                     sn = s;
                     sn.next(p);
-                    tn = rows_part(p, sn, n + s.w * s.units(), w, r);
+                    tn = rows_part(p, sn, n + s.jobs(), w, r);
                     rows_query<D, kFmt>(p, tn, qtile, r);
                 }
                 if (t.any) {   // warps whose 32 rows are all past the tile leave the weights as they are: rows do not mix
@@ -1327,7 +1345,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
         __syncwarp();
         tm_fence_before();   // the accumulator has been read before the next segment's first product
         unit0 += s.units();
-        n += s.w * s.units();
+        n += s.jobs();
         s = sn;
         t = tn;
     }
@@ -1410,12 +1428,12 @@ template <int D>
 struct RowsMerge {
     static constexpr int V = D / 32, kBatch = 4;
     float M = -INFINITY, L = 0.0f, O[V] = {};
-    // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose weighted units start
+    // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose first unit begins
     // at `start`: CTAs cf .. cl, both warpgroups' where the units went to one and the other.
     __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, int both, long long q,
                                          long long item, int r, int lane) {
         if (per <= 0) return;
-        const int w = both ? 2 : 1, shares = both ? 1 : 2;
+        const int w = both ? kRowsBothCost : kRowsOneCost, shares = both ? 1 : 2;
         const int cf = (int)rows_div(start, q), cl = (int)rows_div(start + (long long)(per - 1) * w, q), n = (cl - cf + 1) * shares;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kBatch) {
@@ -1428,8 +1446,8 @@ struct RowsMerge {
                 l[k] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[k][e] = 0.0f;
-                // (a CTA with an odd range of one weighted unit may hold no start of a unit of weight 2)
-                const bool has = ceil_half(max(c * q - start, 0LL), w) < ceil_half(min((c + 1) * q - start, (long long)per * w), w);
+                // (no unit need begin in a short range)
+                const bool has = rows_begun(c * q - start, w, per) < rows_begun((c + 1) * q - start, w, per);
                 const long long slot = rows_slot(p, c, item, c == cf);
                 if (i < n && has && (own || slot < p.rec_slots)) {
                     const int g = both ? r >> 7 : i & 1, rr = both ? r & 127 : r;
@@ -1505,11 +1523,12 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
     if (g >= 0) {
         const RowsList r = rows_list(p, g);
         const long long first = p.plan->list[g].first, tile0 = p.plan->list[g].tile0;
-        const int rr = (row - rows_first(p, g)) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? 2 : r.last;
-        acc.take(p, false, first + (long long)mt * p.hkv * r.per * 2 + (long long)j * r.per * w, r.per, w == 2, q,
+        const int rr = (row - rows_first(p, g)) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? kRowsBothCost : r.last;
+        acc.take(p, false, first + (long long)mt * p.hkv * rows_cost(p, r.per, kRowsBothCost) + j * rows_cost(p, r.per, w) + p.head,
+                 r.per, w == kRowsBothCost, q,
                  (tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
     }
-    acc.take(p, true, own_first + (long long)j * per, per, 0, q, (long long)row * p.hkv + j, hh, lane);
+    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, 0, q, (long long)row * p.hkv + j, hh, lane);
     acc.store(p, (size_t)row * p.hq + h, lane);
 }
 
@@ -1534,10 +1553,10 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     if (c.u0 >= c.u1 || c.start >= c.u0) return;
     const RowsList r = rows_list(p, c.list);
     const int first = rows_first(p, c.list), heads = (rows_first(p, c.list + 1) - first) * p.G;
-    const int w = c.mt < r.tiles - 1 ? 2 : r.last, rr = c.mt * kRowsTile + x;
+    const int w = c.mt < r.tiles - 1 ? kRowsBothCost : r.last, rr = c.mt * kRowsTile + x;
     if (x >= kRowsTile || rr >= heads || c.start < b * q || c.start + (long long)(r.per - 1) * w < c.u0) return;
     RowsMerge<D> acc;
-    acc.take(p, false, c.start, r.per, w == 2, q, (c.tile0 + c.mt) * p.hkv + c.j, x, lane);
+    acc.take(p, false, c.start, r.per, w == kRowsBothCost, q, (c.tile0 + c.mt) * p.hkv + c.j, x, lane);
     acc.store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)c.j * p.G + rr % p.G, lane);
 }
 
