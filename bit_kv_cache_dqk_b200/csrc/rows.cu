@@ -305,7 +305,8 @@ dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost
     }
     const int rows = (int)std::min<long long>(kRowsTile, (long long)p.total_rows * p.G);
     return launch_overlapped(k_rows_merge_items<D>,
-                             dim3((unsigned)(p.num_ctas - 1 + std::min(p.n_groups, 32)), (rows + kRowsMergeWarps - 1) / kRowsMergeWarps),
+                             dim3((unsigned)(p.num_ctas - 1 + std::min(p.n_groups, 32)),
+                                  (rows + kRowsMergeWarps * kRowsMergeHeads - 1) / (kRowsMergeWarps * kRowsMergeHeads)),
                              32 * kRowsMergeWarps, 0, a.stream, p);
 }
 

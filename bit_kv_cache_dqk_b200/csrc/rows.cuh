@@ -1426,18 +1426,46 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsMerge {
-    static constexpr int V = D / 32, kBatch = 4;
+    static constexpr int V = D / 32, kBatch = 8;
     float M = -INFINITY, L = 0.0f, O[V] = {};
+    static __device__ __forceinline__ void load(const float *rec, int lane, float &m, float &l, float (&o)[V]) {
+        m = __ldcg(rec);
+        l = __ldcg(rec + 1);
+        if constexpr (V == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(rec + kRecHead) + lane);
+            o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+        } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(rec + kRecHead) + lane);
+            o[0] = x.x; o[1] = x.y;
+        }
+    }
+    // The reference moves to `to` where that is larger.
+    __device__ __forceinline__ void scale(float to) {
+        to = fmaxf(M, to);
+        const float sc = exp2f(M - base(to));   // 0 while M is -inf
+        M = to;
+        L *= sc;
+#pragma unroll
+        for (int e = 0; e < V; ++e) O[e] *= sc;
+    }
+    static __device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.0f : m; }
+    __device__ __forceinline__ void add(float m, float l, const float (&o)[V]) {
+        const float f = exp2f(m - base(M));
+        const bool none = m == -INFINITY && l == 0.0f;   // an empty record: its o was not written
+        L = fmaf(f, l, L);
+#pragma unroll
+        for (int e = 0; e < V; ++e) O[e] = none ? O[e] : fmaf(f, o[e], O[e]);
+    }
     // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose first unit begins
     // at `start`: CTAs cf .. cl, both warpgroups' where the units went to one and the other.
-    __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, int both, long long q,
+    __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, bool both, long long q,
                                          long long item, int r, int lane) {
         if (per <= 0) return;
         const int w = both ? kRowsBothCost : kRowsOneCost, shares = both ? 1 : 2;
         const int cf = (int)rows_div(start, q), cl = (int)rows_div(start + (long long)(per - 1) * w, q), n = (cl - cf + 1) * shares;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float m[kBatch], l[kBatch], o[kBatch][V];
+            float m[kBatch], l[kBatch], o[kBatch][V], to = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k;
@@ -1451,35 +1479,16 @@ struct RowsMerge {
                 const long long slot = rows_slot(p, c, item, c == cf);
                 if (i < n && has && (own || slot < p.rec_slots)) {
                     const int g = both ? r >> 7 : i & 1, rr = both ? r & 127 : r;
-                    const float *rec = own ? p.own_rec + rows_own_rec(c + item, g, p.G, rr) * rec_stride(D)
-                                           : p.rec + rows_rec(slot, g, rr) * rec_stride(D);
-                    m[k] = __ldcg(rec);
-                    l[k] = __ldcg(rec + 1);
-                    if constexpr (V == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(rec + kRecHead) + lane);
-                        o[k][0] = x.x; o[k][1] = x.y; o[k][2] = x.z; o[k][3] = x.w;
-                    } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(rec + kRecHead) + lane);
-                        o[k][0] = x.x; o[k][1] = x.y;
-                    }
+                    load(own ? p.own_rec + rows_own_rec(c + item, g, p.G, rr) * rec_stride(D)
+                             : p.rec + rows_rec(slot, g, rr) * rec_stride(D),
+                         lane, m[k], l[k], o[k]);
                 }
             }
-            float to = M;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) to = fmaxf(to, m[k]);
-            const float base = to == -INFINITY ? 0.0f : to, sc = exp2f(M - base);   // 0 while M is -inf
-            M = to;
-            L *= sc;
+            scale(to);
 #pragma unroll
-            for (int e = 0; e < V; ++e) O[e] *= sc;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float f = exp2f(m[k] - base);
-                const bool none = m[k] == -INFINITY && l[k] == 0.0f;   // an empty record: its o was not written
-                L = fmaf(f, l[k], L);
-#pragma unroll
-                for (int e = 0; e < V; ++e) O[e] = none ? O[e] : fmaf(f, o[k][e], O[e]);
-            }
+            for (int k = 0; k < kBatch; ++k) add(m[k], l[k], o[k]);
         }
     }
     __device__ __forceinline__ void store(const RowsParams &p, size_t head, int lane) const {
@@ -1528,23 +1537,27 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
                  r.per, w == kRowsBothCost, q,
                  (tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
     }
-    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, 0, q, (long long)row * p.hkv + j, hh, lane);
+    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, false, q, (long long)row * p.hkv + j, hh, lane);
     acc.store(p, (size_t)row * p.hq + h, lane);
 }
 
-// Without own lists, CTA (b, y): row heads 8 y .. 8 y + 7 of the item that begins in CTA b of the row kernel and
-// goes on in the next one (every other item's outputs are written already), a warp each; the CTAs behind those zero
-// the rows of groups without any token.
+// Without own lists, CTA (b, y): row heads 8 y .., a warp each, and those 8 gridDim.y further on, of the item that
+// begins in CTA b of the row kernel and goes on in the next one (every other item's outputs are written already); the
+// CTAs behind those zero the rows of groups without any token.
+// What bounds it is the arithmetic of the items and records, which the warp's row heads share (cross attention of 4 x
+// 1024 queries over 4096 states, all kernels, with 1, 2 and 4 of them: 213, 204, 208 us).
+constexpr int kRowsMergeHeads = 2;
 template <int D>
 __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const __grid_constant__ RowsParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, x = blockIdx.y * kRowsMergeWarps + warp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, x0 = blockIdx.y * kRowsMergeWarps + warp;
+    const int step = (int)gridDim.y * kRowsMergeWarps;
     grid_dependency_wait();
     if (b >= p.num_ctas - 1) {
         for (int g = b - (p.num_ctas - 1); g < p.n_groups; g += (int)gridDim.x - (p.num_ctas - 1)) {
             if (rows_list(p, g).per > 0) continue;
             const size_t at = (size_t)rows_first(p, g) * p.hq, n = (size_t)max(rows_first(p, g + 1) - rows_first(p, g), 0) * p.hq;
             const RowsMerge<D> zero;
-            for (size_t i = x; i < n; i += (size_t)gridDim.y * kRowsMergeWarps) zero.store(p, at + i, lane);
+            for (size_t i = x0; i < n; i += step) zero.store(p, at + i, lane);
         }
         return;
     }
@@ -1552,12 +1565,47 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     const long long q = p.plan->q;
     if (c.u0 >= c.u1 || c.start >= c.u0) return;
     const RowsList r = rows_list(p, c.list);
-    const int first = rows_first(p, c.list), heads = (rows_first(p, c.list + 1) - first) * p.G;
-    const int w = c.mt < r.tiles - 1 ? kRowsBothCost : r.last, rr = c.mt * kRowsTile + x;
-    if (x >= kRowsTile || rr >= heads || c.start < b * q || c.start + (long long)(r.per - 1) * w < c.u0) return;
-    RowsMerge<D> acc;
-    acc.take(p, false, c.start, r.per, w == kRowsBothCost, q, (c.tile0 + c.mt) * p.hkv + c.j, x, lane);
-    acc.store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)c.j * p.G + rr % p.G, lane);
+    const int first = rows_first(p, c.list), w = c.mt < r.tiles - 1 ? kRowsBothCost : r.last;
+    if (c.start < b * q || c.start + (long long)(r.per - 1) * w < c.u0) return;
+    const int heads = min((rows_first(p, c.list + 1) - first) * p.G - c.mt * kRowsTile, kRowsTile);
+    if (x0 >= heads) return;
+    RowsMerge<D> acc[kRowsMergeHeads];
+    const bool both = w == kRowsBothCost;
+    const long long item = (c.tile0 + c.mt) * p.hkv + c.j;
+    const int cl = (int)rows_div(c.start + (long long)(r.per - 1) * w, q);
+    const int shares = both ? 1 : 2, n = (cl - b + 1) * shares;
+    for (int i0 = 0; i0 < n; i0 += 2) {   // two records of every row head at a time
+        float m[2][kRowsMergeHeads], l[2][kRowsMergeHeads], o[2][kRowsMergeHeads][RowsMerge<D>::V];
+        bool has[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int a = b + (i0 + e) / shares, g = (i0 + e) % shares;
+            const long long slot = rows_slot(p, a, item, a == b);
+            has[e] = i0 + e < n && slot < p.rec_slots &&
+                     rows_begun(a * q - c.start, w, r.per) < rows_begun((a + 1) * q - c.start, w, r.per);
+            if (!has[e]) continue;
+#pragma unroll
+            for (int k = 0; k < kRowsMergeHeads; ++k) {
+                const int x = min(x0 + k * step, heads - 1);
+                RowsMerge<D>::load(p.rec + (both ? rows_rec(slot, x >> 7, x & 127) : rows_rec(slot, g, x)) * rec_stride(D), lane,
+                                   m[e][k], l[e][k], o[e][k]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (!has[e]) continue;
+#pragma unroll
+            for (int k = 0; k < kRowsMergeHeads; ++k) {
+                acc[k].scale(m[e][k]);
+                acc[k].add(m[e][k], l[e][k], o[e][k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsMergeHeads; ++k) {
+        const int x = x0 + k * step, rr = c.mt * kRowsTile + x;
+        if (x < heads) acc[k].store(p, (size_t)(first + rr / p.G) * p.hq + (size_t)c.j * p.G + rr % p.G, lane);
+    }
 }
 
 }  // namespace dqk
