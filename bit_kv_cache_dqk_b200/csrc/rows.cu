@@ -275,6 +275,7 @@ struct RowsCall {
     void *ws;
     size_t ws_bytes;
     cudaStream_t stream;
+    bool zero_rest;                       // rows of no group: zeros, or left as they were
 };
 
 template <int D, int kFmt, int NS, bool VCH0>
@@ -383,6 +384,7 @@ dqk_status run_rows(const RowsCall &a) {
     p.rec = reinterpret_cast<float *>(ws + P.off_rec);
     p.own_rec = reinterpret_cast<float *>(ws + P.off_own);
     p.slot_pairs = P.slot_pairs;
+    p.zero_rest = a.zero_rest;
     p.rec_slots = P.slots;
     p.out = a.out;
     p.out_dtype = (int)a.out_dtype;
@@ -440,7 +442,7 @@ dqk_status dqk_prefix_decode(const dqk_layer_desc *layer, const void *q, dqk_dty
     if (st != DQK_OK) return st;
     return run_rows(RowsCall{layer, true, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
                              max_prefix_pages, max_pages ? batch : 0, seq_lens, page_table, max_pages, sparsity_pct, out,
-                             out_dtype, sel_out, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)});
+                             out_dtype, sel_out, workspace, workspace_bytes, static_cast<cudaStream_t>(stream), true});
 }
 
 dqk_status dqk_bf16_prefix_decode(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch, int n_prefixes,
@@ -453,7 +455,7 @@ dqk_status dqk_bf16_prefix_decode(const dqk_layer_desc *layer, const void *q, dq
     if (st != DQK_OK) return st;
     return run_rows(RowsCall{layer, false, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
                              max_prefix_pages, max_pages ? batch : 0, seq_lens, page_table, max_pages, 0, out, out_dtype,
-                             nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)});
+                             nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream), true});
 }
 
 dqk_status dqk_bf16_cross_attention(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch, int total_q,
@@ -464,7 +466,7 @@ dqk_status dqk_bf16_cross_attention(const dqk_layer_desc *layer, const void *q, 
     if (batch <= 0 || total_q <= 0 || max_pages <= 0) return DQK_ERR_INVALID_ARG;
     return run_rows(RowsCall{layer, false, q, q_dtype, total_q, batch, q_start, kv_lens, page_table, max_pages, 0, nullptr,
                              nullptr, 0, 0, out, out_dtype, nullptr, workspace, workspace_bytes,
-                             static_cast<cudaStream_t>(stream)});
+                             static_cast<cudaStream_t>(stream), false});
 }
 
 }  // extern "C"

@@ -76,6 +76,7 @@ struct RowsParams {
     struct RowsPlan *plan;      // what the merge needs of the split (written by the row kernel)
     float *rec, *own_rec;       // split records of the groups' and of the own items
     bool slot_pairs;            // see rows_slot
+    bool zero_rest;             // rows of no group become zeros
     long long rec_slots;        // slots `rec` holds (row_start out of order could ask for more)
     void *out;
     int out_dtype;
@@ -1543,7 +1544,7 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
 
 // Without own lists, CTA (b, y): row heads 8 y .., a warp each, and those 8 gridDim.y further on, of the item that
 // begins in CTA b of the row kernel and goes on in the next one (every other item's outputs are written already); the
-// CTAs behind those zero the rows of groups without any token.
+// CTAs behind those zero the rows of groups without any token (and, zero_rest, of no group).
 // What bounds it is the arithmetic of the items and records, which the warp's row heads share (cross attention of 4 x
 // 1024 queries over 4096 states, all kernels, with 1, 2 and 4 of them: 213, 204, 208 us).
 constexpr int kRowsMergeHeads = 2;
@@ -1553,9 +1554,12 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     const int step = (int)gridDim.y * kRowsMergeWarps;
     grid_dependency_wait();
     if (b >= p.num_ctas - 1) {
-        for (int g = b - (p.num_ctas - 1); g < p.n_groups; g += (int)gridDim.x - (p.num_ctas - 1)) {
-            if (rows_list(p, g).per > 0) continue;
-            const size_t at = (size_t)rows_first(p, g) * p.hq, n = (size_t)max(rows_first(p, g + 1) - rows_first(p, g), 0) * p.hq;
+        const int n_runs = p.n_groups + (p.zero_rest ? 2 : 0);   // and the rows before the first group, behind the last
+        for (int g = b - (p.num_ctas - 1); g < n_runs; g += (int)gridDim.x - (p.num_ctas - 1)) {
+            if (g < p.n_groups && rows_list(p, g).per > 0) continue;
+            const int r0 = g <= p.n_groups ? rows_first(p, g) : 0;
+            const int r1 = g < p.n_groups ? rows_first(p, g + 1) : g == p.n_groups ? p.total_rows : rows_first(p, 0);
+            const size_t at = (size_t)r0 * p.hq, n = (size_t)max(r1 - r0, 0) * p.hq;
             const RowsMerge<D> zero;
             for (size_t i = x0; i < n; i += step) zero.store(p, at + i, lane);
         }
