@@ -26,6 +26,7 @@ __host__ __device__ constexpr size_t query_rows_smem() {
 //   cover channels down to 2^-28 of it;
 //   scale [row][hq] = 2^-k log2(e)/sqrt(d), which the scores are multiplied by.
 // A query of zeros (or subnormals) becomes a row of zeros: every score 0.
+// Bound by latency (T_Q[j] in, the fp64 sums, the selection's rounds): 8 us for 16 rows of 8 kv heads, 17 us for 64.
 template <int D, int G, int RB>
 __global__ void __launch_bounds__(kQueryThreads) k_query_rows(
     const float *__restrict__ t_q, const void *__restrict__ q, int dtype, int rows, int hq, int pct, float qscale,

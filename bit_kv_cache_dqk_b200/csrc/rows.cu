@@ -96,12 +96,12 @@ dqk_status rope_grid(RopeParams &p, int rows, unsigned &gx) {
     return DQK_OK;
 }
 
-template <int D, int TT>
+template <int D>
 dqk_status run_rope_b16(RopeParams &p, cudaStream_t s) {
     unsigned gx = 0;
-    const dqk_status st = rope_grid(p, TT, gx);
+    const dqk_status st = rope_grid(p, kRopeTile, gx);
     if (st != DQK_OK) return st;
-    k_rope_append_b16<D, TT><<<gx, kRopeThreads, 0, s>>>(p);
+    k_rope_append_b16<D><<<gx, kRopeThreads, 0, s>>>(p);
     return launch_status();
 }
 
@@ -179,9 +179,7 @@ dqk_status dqk_bf16_rope_append(DQK_ROPE_ARGS) {
     RopeParams p;
     st = check_rope(a, p);
     if (st != DQK_OK || max_new == 0) return st;
-    const bool tile = max_new >= 4;
-    if (layer->head_dim == 128) return tile ? run_rope_b16<128, 4>(p, a.stream) : run_rope_b16<128, 1>(p, a.stream);
-    return tile ? run_rope_b16<64, 4>(p, a.stream) : run_rope_b16<64, 1>(p, a.stream);
+    return layer->head_dim == 128 ? run_rope_b16<128>(p, a.stream) : run_rope_b16<64>(p, a.stream);
 }
 
 }  // extern "C"
@@ -323,8 +321,9 @@ dqk_status launch_query_rows(const RowsCall &a, const RowsParams &p, int dev, ui
 
 template <int D, int G>
 dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float *scale) {
-    // four rows per staged transform once there are CTAs for every SM twice over without it
-    return (long long)p.total_rows * p.hkv > 2 * 148 ? launch_query_rows<D, G, 4>(a, p, dev, rows, scale)
+    // four rows per staged transform once one row each makes more than three CTAs per SM: the whole decode with 1 and
+    // 4 (us; 8 kv heads, 1024 shared tokens) 38 and 42 at 32 rows, 49 and 51 at 48, 63 and 59 at 64, 97 and 93 at 128
+    return (long long)p.total_rows * p.hkv > 3 * 148 ? launch_query_rows<D, G, 4>(a, p, dev, rows, scale)
                                                      : launch_query_rows<D, G, 1>(a, p, dev, rows, scale);
 }
 
