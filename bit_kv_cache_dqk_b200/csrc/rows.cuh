@@ -1261,15 +1261,15 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
         // a list that is whole in this segment (and has nothing to be joined with) becomes outputs here; where
         // its units went to both warpgroups in turn, the second hands its record to the first
         const bool whole = p.n_own == 0 && s.v0 == 0 && s.v1 == s.per;
-        const bool joint = whole && !s.both() && s.per > 1;
         const long long item = s.item(p), slot = rows_slot(p, cta, item, s.v0 == 0);
+        const bool fits = s.own(p) || slot < p.rec_slots, split = !s.both() && s.per > 1, joint = whole && split && fits;
         if (w == 1 && pending && (joint || !whole)) {   // the first warpgroup has read the record before it is written again
             ok = __all_sync(0xffffffffu, rows_wait(&B.read, rn & 1, B, p.wait_ns));
             ++rn;
             if (!ok) return;
             pending = false;
         }
-        if (whole && !(joint && w == 1)) {
+        if (whole && (!split || (fits && w == 0))) {
             float f = 1.0f, f1 = 0.0f;
             const float *other = p.rec + rows_rec(slot, 1, r) * rec_stride(D);
             if (joint) {
@@ -1323,7 +1323,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             }
             __syncwarp();
             if (joint && lane == 0) mbar_arrive(&B.read);
-        } else if (s.own(p) || slot < p.rec_slots) {
+        } else if (fits) {
             float *rec = (s.own(p) ? p.own_rec + rows_own_rec(cta + item, w, p.G, r) * rec_stride(D)
                                    : p.rec + rows_rec(slot, w, r) * rec_stride(D));
             if (t.valid) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);   // no unit of this segment: (-inf, 0) alone

@@ -59,3 +59,28 @@ def test_workspace_of_the_largest_call_serves_smaller_ones():
             probe = Q.layer_desc(128, 4 * hkv, hkv, 256, 256, 256, 4096)
             sizes = [size(probe, rows, 1, 64, own) for own in (0, 1, 9, 64)]
             assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_groups_that_overlap_are_reported():
+    """More row tiles than ascending starts could have: an error, no access past the workspace."""
+    rows, times = 650, 20
+    L = R.Lists("bf16", [[300] * (2 * times - 1)], 8, 1, 128, seed=9)
+    q = queries(L, rows)
+    q_start = [0, rows] * times
+    ws_size = Q.dqk_bf16_cross_attention_workspace_size(L.desc, 2 * times - 1, rows, L.tables[0].shape[1])
+    guard = 1 << 20
+    ws = torch.full((ws_size + guard,), 0x5A, dtype=torch.uint8, device=L.dev)
+    qd = R.as_dtype(q, "bf16").to(L.dev)
+    out = torch.zeros((rows, 8, 128), device=L.dev)
+    starts, lens, table = torch.tensor(q_start, dtype=torch.int32, device=L.dev), L.lens_dev(0), L.table_dev(0)
+    Q.dqk_bf16_cross_attention(L.desc, qd, Q.DQK_BF16, 2 * times - 1, rows, starts, lens, table, table.shape[1], out, Q.DQK_F32,
+                               ws, ws_size)
+    torch.cuda.synchronize()
+    assert Q.dqk_last_device_error() == Q.DQK_ERR_DEVICE_BOUNDS
+    assert (ws[ws_size:] == 0x5A).all()
+    one = R.Lists("bf16", [[300]], 8, 1, 128, seed=9)       # the next call is not affected
+    got, = [one.cross(q[:40], "bf16", [0, 40])]
+    torch.cuda.synchronize()
+    assert Q.dqk_last_device_error() == Q.DQK_OK
+    got = got[0] if isinstance(got, tuple) else got
+    assert torch.isfinite(got.float()).all()
