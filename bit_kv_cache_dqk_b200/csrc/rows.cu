@@ -280,14 +280,14 @@ template <int D, int kFmt, int NS, bool VCH0>
 dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost &P, int dev) {
     using T = RowsShape<D, kFmt>;
     // shared memory: 1024 bytes of alignment, the query tiles, the rings
-    constexpr size_t kBudget = 227 * 1024 - 1024 - sizeof(RowsBars) - 2 * T::kParts * T::kTile;
+    constexpr size_t kRoom = 227 * 1024 - 1024 - sizeof(RowsBars) - 2 * T::kParts * T::kTile;
     // a key tile is free again as soon as its scores are formed, a value tile only after its unit's weights: with an
     // odd number the values have one more
-    const int tiles = T::kInt2 ? 4 : (int)std::min<size_t>(kRowsMaxTiles, kBudget / T::kTile);
+    const int tiles = T::kInt2 ? 4 : (int)std::min<size_t>(kRowsMaxTiles, kRoom / T::kTile);
     p.ktiles = tiles / 2;
     p.vtiles = tiles - p.ktiles;
     // page flags: at most kRowsFlags units between their copies and the softmax
-    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kBudget - 4 * T::kTile) / (kRowsPages * P.bb)) : 0;
+    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kRoom - 4 * T::kTile) / (kRowsPages * P.bb)) : 0;
     const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb;
     dqk_status st = prepare_kernel<k_rows<D, kFmt, NS, VCH0>>(dev, smem, T::kThreads);
     if (st != DQK_OK) return st;
