@@ -276,7 +276,7 @@ struct RowsCall {
     bool zero_rest;                       // rows of no group: zeros, or left as they were
 };
 
-template <int D, int kFmt, int NS, bool VCH0>
+template <int D, int kFmt, int kW, int NS, bool VCH0>
 dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost &P, int dev) {
     using T = RowsShape<D, kFmt>;
     // shared memory: 1024 bytes of alignment, the query tiles, the rings
@@ -289,14 +289,14 @@ dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost
     // page flags: at most kRowsFlags units between their copies and the softmax
     p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kRoom - 4 * T::kTile) / (kRowsPages * P.bb)) : 0;
     const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb;
-    dqk_status st = prepare_kernel<k_rows<D, kFmt, NS, VCH0>>(dev, smem, T::kThreads);
+    dqk_status st = prepare_kernel<k_rows<D, kFmt, kW, NS, VCH0>>(dev, smem, T::kThreads);
     if (st != DQK_OK) return st;
     CUtensorMap map = {};
     if (!T::kInt2) {
         st = pool_map(a.layer, map);
         if (st != DQK_OK) return st;
     }
-    st = launch_overlapped(k_rows<D, kFmt, NS, VCH0>, dim3(p.num_ctas), T::kThreads, smem, a.stream, p, map);
+    st = launch_overlapped(k_rows<D, kFmt, kW, NS, VCH0>, dim3(p.num_ctas), T::kThreads, smem, a.stream, p, map);
     if (st != DQK_OK) return st;
     if (p.n_own > 0) {
         return launch_overlapped(k_rows_merge<D>, dim3((unsigned)p.total_rows, (p.hq + kRowsMergeWarps - 1) / kRowsMergeWarps),
@@ -330,8 +330,11 @@ dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint1
 template <int D>
 dqk_status run_rows_d(const RowsCall &a, const RowsPlanHost &P, RowsParams &p, int dev) {
     if (!a.int2) {
-        return a.q_dtype == DQK_BF16 ? run_rows_kernels<D, 0, 1, false>(a, p, P, dev)
-                                     : run_rows_kernels<D, 1, 1, false>(a, p, P, dev);
+        if (a.out_dtype == DQK_BF16)
+            return a.q_dtype == DQK_BF16 ? run_rows_kernels<D, 0, 1, 1, false>(a, p, P, dev)
+                                         : run_rows_kernels<D, 1, 1, 1, false>(a, p, P, dev);
+        return a.q_dtype == DQK_BF16 ? run_rows_kernels<D, 0, 2, 1, false>(a, p, P, dev)
+                                     : run_rows_kernels<D, 1, 2, 1, false>(a, p, P, dev);
     }
     char *ws = static_cast<char *>(a.ws);
     uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
@@ -344,10 +347,10 @@ dqk_status run_rows_d(const RowsCall &a, const RowsPlanHost &P, RowsParams &p, i
     p.q = rows;
     p.q_scale = scale;
     const bool one = a.layer->group_size == D, v0 = a.layer->v_ch0_protect != 0;
-    if (one) return v0 ? run_rows_kernels<D, 2, 1, true>(a, p, P, dev)
-                       : run_rows_kernels<D, 2, 1, false>(a, p, P, dev);
-    return v0 ? run_rows_kernels<D, 2, D / kGroup, true>(a, p, P, dev)
-              : run_rows_kernels<D, 2, D / kGroup, false>(a, p, P, dev);
+    if (one) return v0 ? run_rows_kernels<D, 2, 1, 1, true>(a, p, P, dev)
+                       : run_rows_kernels<D, 2, 1, 1, false>(a, p, P, dev);
+    return v0 ? run_rows_kernels<D, 2, 1, D / kGroup, true>(a, p, P, dev)
+              : run_rows_kernels<D, 2, 1, D / kGroup, false>(a, p, P, dev);
 }
 
 dqk_status run_rows(const RowsCall &a) {

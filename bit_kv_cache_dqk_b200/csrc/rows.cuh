@@ -895,7 +895,7 @@ __device__ __forceinline__ void rows_tails(const RowsParams &p, RowsBars &B, uns
 // The matrix thread of warpgroup w.  Half h of the next job's scores follows half h of this
 // job's outputs, whose weights lie in the same columns.  Tiles of units that are the other
 // warpgroup's alone are released here too (two arrivals free a tile).
-template <int D, int kFmt>
+template <int D, int kFmt, int kW>
 __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *qmem,
                                             uint32_t tmem, int w) {
     using T = RowsShape<D, kFmt>;
@@ -979,6 +979,7 @@ __device__ __forceinline__ void rows_matrix(const RowsParams &p, RowsBars &B, un
                 if (s >= pairs) break;
                 const uint32_t off = (uint32_t)(T::kInt2 ? h * (D * 128) + s * 32 : 2 * s * T::kPageBytes + h * 1024) >> 4;
                 mma_ts<T::kGroupKv>(tO, tS + 64 * h + 8 * s, b + off, T::kIdescO, h > 0 || s > 0 ? 1u : acc);
+                if constexpr (kW == 2) mma_ts<T::kGroupKv>(tO, tS + 64 * h + 32 + 8 * s, b + off, T::kIdescO, 1u);
             }
             mma_commit(&B.o_step[w]);
             if (h == 0) {
@@ -1031,9 +1032,16 @@ __device__ __forceinline__ void rows_mask(uint32_t tS, int nv, uint32_t have, in
     tm_wait_st();
 }
 
-// 16 scores of a thread's row -> weights 2^(x qs - base), packed in pairs; their sum is added to
-// s0, s1 and their largest score taken into m0, m1.
-template <bool F16>
+// Two weights as a pair of operands: high parts, and (kW == 2) what those leave, 2^-8 of it off.
+template <bool F16, int kW>
+__device__ __forceinline__ void rows_pack(float2 y, uint32_t &hi, uint32_t &lo) {
+    hi = F16 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
+    if constexpr (kW == 2) lo = pack_bf16x2(y.x - __uint_as_float(hi << 16), y.y - __uint_as_float(hi & 0xffff0000u));
+}
+
+// 16 scores of a thread's row -> weights 2^(x qs - base), packed in pairs (kW == 2: low parts 32 words on);
+// their sum is added to s0, s1 and their largest score taken into m0, m1.
+template <bool F16, int kW>
 __device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2, float2 b2, uint32_t *pk, float2 &s0, float2 &s1,
                                              float &m0, float &m1) {
     float2 e[8], y[8];
@@ -1047,8 +1055,8 @@ __device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2,
         m1 = max3(m1, __uint_as_float(u[2 * i + 2]), __uint_as_float(u[2 * i + 3]));
         s0 = add2(s0, y[i]);
         s1 = add2(s1, y[i + 1]);
-        pk[i] = F16 ? pack_f16x2(y[i].x, y[i].y) : pack_bf16x2(y[i].x, y[i].y);
-        pk[i + 1] = F16 ? pack_f16x2(y[i + 1].x, y[i + 1].y) : pack_bf16x2(y[i + 1].x, y[i + 1].y);
+        rows_pack<F16, kW>(y[i], pk[i], pk[i + (kW - 1) * 32]);
+        rows_pack<F16, kW>(y[i + 1], pk[i + 1], pk[i + 1 + (kW - 1) * 32]);
     }
 }
 
@@ -1084,18 +1092,19 @@ __device__ __forceinline__ float rows_largest(uint32_t tS, float qs) {
 }
 
 // The weights of a thread's row for half a unit: S (64 columns at tS) becomes P~
-// (packed pairs, its first 32 columns), and the reference m and the sum l of the row follow.  A half
+// (packed pairs: its first 32 columns, low parts in the others), and the reference m and the sum l of the row follow.  A half
 // whose scores pass the reference by more than the slack (rare) is taken again after the reference
 // has moved and what was summed -- l, and the accumulator, once `settled` has waited for it -- has been rescaled.
-template <int D, bool F16, typename Settled>
+template <int D, bool F16, int kW, typename Settled>
 __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, float lift, float &m, float &l,
                                           Settled settled) {
-    uint32_t pk[32];
+    uint32_t pk[32 * kW];
     const float2 q2 = make_float2(qs, qs);
     float base = (m == -INFINITY ? 0.0f : m) - lift;
     float2 b2 = make_float2(-base, -base), s0 = make_float2(0.0f, 0.0f), s1 = s0;
     float m0 = -INFINITY, m1 = -INFINITY;
-    constexpr int kAtOnce = F16 ? 2 : 4;   // 16-column loads in registers together (INT2: 128 registers a thread)
+    // 16-column loads in registers together (INT2 has 128 registers a thread, and low parts take theirs)
+    constexpr int kAtOnce = F16 || kW == 2 ? 2 : 4;
 #pragma unroll
     for (int c0 = 0; c0 < 4; c0 += kAtOnce) {
         uint32_t x[kAtOnce][16];
@@ -1104,7 +1113,7 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, 
 #pragma unroll
         for (int c = 0; c < kAtOnce; ++c) tm_ready16(x[c]);
 #pragma unroll
-        for (int c = 0; c < kAtOnce; ++c) rows_weights<F16>(x[c], q2, b2, pk + 8 * (c0 + c), s0, s1, m0, m1);
+        for (int c = 0; c < kAtOnce; ++c) rows_weights<F16, kW>(x[c], q2, b2, pk + 8 * (c0 + c), s0, s1, m0, m1);
     }
     const float mx = fmaxf(m0, m1) * qs;
     const bool move = valid && mx > m + kRowsSlack;   // (lanes without a row hold anything)
@@ -1124,12 +1133,12 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, 
             uint32_t y[16];
             tm_ld16(tS + 16 * c, y);
             tm_ready16(y);
-            rows_weights<F16>(y, q2, b2, pk + 8 * c, s0, s1, m0, m1);
+            rows_weights<F16, kW>(y, q2, b2, pk + 8 * c, s0, s1, m0, m1);
         }
     }
     l += (s0.x + s0.y) + (s1.x + s1.y);
-    tm_st16(tS, pk);
-    tm_st16(tS + 16, pk + 16);
+#pragma unroll
+    for (int i = 0; i < 2 * kW; ++i) tm_st16(tS + 16 * i, pk + 16 * i);
     tm_wait_st();
     return true;
 }
@@ -1179,7 +1188,7 @@ __device__ __forceinline__ void rows_query(const RowsParams &p, const RowsPart &
 }
 
 // Softmax warpgroup w.
-template <int D, int kFmt>
+template <int D, int kFmt, int kW>
 __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, unsigned char *qmem, uint32_t tmem, int w, int cta) {
     using T = RowsShape<D, kFmt>;
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
@@ -1236,7 +1245,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     if (none) m = ceilf(rows_largest(tS, qs));   // no reference yet
                     // the half before this one may still be on its way into the accumulator (the one before that is not:
                     // these scores lie where its weights were)
-                    ok = rows_half<D, kFmt == 2>(tS + 64 * h, tO, t.valid, qs, T::kLift, m, l, [&]() {
+                    ok = rows_half<D, kFmt == 2, kW>(tS + 64 * h, tO, t.valid, qs, T::kLift, m, l, [&]() {
                         if (none) return 0;
                         if (!__all_sync(0xffffffffu, rows_wait(&B.o_step[w], (pn - 1) & 1u, B, p.wait_ns))) return -1;
                         tm_fence_after();
@@ -1360,7 +1369,13 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
     }
 }
 
-template <int D, int kFmt, int NS, bool VCH0>
+// kFmt: BF16 cache with BF16 (0) or fp32 queries (1), INT2 cache (2); kW: parts of a softmax weight.
+// A BF16 output is rounded by half a step, 2^-8, itself, and so may the weights be, each for itself (against
+// 64 bits 0.0023 where the output's rounding alone leaves 0.0017); an fp32 output gets weights of two parts, 2^-16, as in
+// dqk_bf16_decode (3e-6 where one part leaves 0.0017).  The second product costs 16 % where the softmax warpgroups
+// bound (up to 1024 queries over up to 4096 states, fp32 out: 225 and 262 us), 6 % on long documents (81 and 86) and
+// up to 2 us of the smallest calls.
+template <int D, int kFmt, int kW, int NS, bool VCH0>
 __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     k_rows(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap map) {
     using T = RowsShape<D, kFmt>;
@@ -1410,11 +1425,11 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     tm_fence_after();
     const uint32_t tmem = B.tmem;
     if (warp < 8) {
-        rows_softmax<D, kFmt>(p, B, qmem, tmem, warp >> 2, blockIdx.x);
+        rows_softmax<D, kFmt, kW>(p, B, qmem, tmem, warp >> 2, blockIdx.x);
     } else {
         if (warp == 8) rows_producer<D, kFmt>(p, &map, B, tiles, raw, lane);
         else if (warp < 11) {
-            if (elect_one()) rows_matrix<D, kFmt>(p, B, tiles, qmem, tmem, warp - 9);
+            if (elect_one()) rows_matrix<D, kFmt, kW>(p, B, tiles, qmem, tmem, warp - 9);
             __syncwarp();
         } else if constexpr (!T::kInt2) {
             rows_tails<D>(p, B, tiles, lane);

@@ -377,7 +377,9 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
  * k^ and v^ rounded once, 2^-11; weights 2^-11) with fp32 accumulation:
  * dequantized magnitudes above fp16's 65504 are outside its range.
  * dqk_bf16_prefix_decode (BF16 cache): fp32 queries are carried as BF16 high +
- * low parts, softmax weights in BF16 (2^-8), accumulation in fp32.
+ * low parts, accumulation in fp32.  With an fp32 `out` so are the softmax weights
+ * (2^-16, as in dqk_bf16_decode); with a BF16 `out`, whose own rounding is 2^-8,
+ * they are rounded to BF16 (2^-8 each).
  * ------------------------------------------------------------------------- */
 size_t dqk_prefix_decode_workspace_size(const dqk_layer_desc *layer, int batch, int n_prefixes, int max_prefix_pages,
                                         int max_pages);
