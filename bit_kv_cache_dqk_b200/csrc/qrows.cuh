@@ -20,17 +20,18 @@ __host__ __device__ constexpr size_t query_rows_smem() {
 }
 
 // CTA per (RB query rows, kv head): T_Q[j] is staged once for the RB G heads.  Row head (row, h) becomes
-//   qr [row][hq][D] fp16 = rne(2^k q'_c) on the kept channels, 0 elsewhere, in the
-//   channel order of the key operand tiles (rows_channel_pos), with
-//   k such that the largest kept |q'_c| lies in [2^14, 2^15): fp16's 11 bits then
+//   qr [row][hq][D] fp16 = rne(2^k q'_c) on the kept channels c >= 1, 0 elsewhere, in
+//   the channel order of the key operand tiles (rows_channel_pos), with
+//   k such that the largest of their |q'_c| lies in [2^14, 2^15): fp16's 11 bits then
 //   cover channels down to 2^-28 of it;
-//   scale [row][hq] = 2^-k log2(e)/sqrt(d), which the scores are multiplied by.
-// A query of zeros (or subnormals) becomes a row of zeros: every score 0.
+//   head [row][hq] = (2^-k, q'_0) log2(e)/sqrt(d): what those scores are multiplied by, and the factor of
+//   the keys' channel 0, which has its own term in fp32 (it is BF16 in the cache, with exponents fp16 lacks).
+// Channels of zeros (or subnormals) become a row of zeros: channel 0 alone gives the scores.
 // Bound by latency (T_Q[j] in, the fp64 sums, the selection's rounds): 8 us for 16 rows of 8 kv heads, 17 us for 64.
 template <int D, int G, int RB>
 __global__ void __launch_bounds__(kQueryThreads) k_query_rows(
     const float *__restrict__ t_q, const void *__restrict__ q, int dtype, int rows, int hq, int pct, float qscale,
-    uint16_t *__restrict__ qr, float *__restrict__ scale, int16_t *__restrict__ sel_out) {
+    uint16_t *__restrict__ qr, float2 *__restrict__ head, int16_t *__restrict__ sel_out) {
     constexpr int NG = D / 32, NH = RB * G, kParts = kQueryThreads / D, kPer = (NH + kParts - 1) / kParts;
     extern __shared__ __align__(16) unsigned char query_rows_mem[];
     unsigned char *sT = query_rows_mem;
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kQueryThreads) k_query_rows(
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const bool kept = (kmask[g] >> lane) & 1u;
-            v[g] = kept ? qp[lane + 32 * g] : 0.0f;
+            v[g] = kept && (g > 0 || lane > 0) ? qp[lane + 32 * g] : 0.0f;
             hm = fmaxf(hm, fabsf(v[g]));
             if (sel_out && kept)
                 sel_out[at * nk + before + __popc(kmask[g] & ((1u << lane) - 1u))] = (int16_t)(lane + 32 * g);
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kQueryThreads) k_query_rows(
 #pragma unroll
         for (int g = 0; g < NG; ++g)
             qr[at * D + rows_channel_pos(lane + 32 * g)] = __half_as_ushort(__float2half_rn(ldexpf(v[g], k)));
-        if (lane == 0) scale[at] = ldexpf(qscale, -k);
+        if (lane == 0) head[at] = make_float2(ldexpf(qscale, -k), qp[0] * qscale);
     }
 }
 

@@ -190,13 +190,13 @@ dqk_status dqk_bf16_rope_append(DQK_ROPE_ARGS) {
 // ---------------------------------------------------------------------------
 namespace {
 
-// Workspace: [query rows fp16 | their scales | plan | group records | own records],
+// Workspace: [query rows fp16 | their scales and factors of channel 0 | plan | group records | own records],
 // sections 256-byte aligned.
 struct RowsPlanHost {
     int d, G, bb;
     bool slot_pairs;
     long long slots, own_slots, tiles;
-    size_t off_scale, off_plan, off_rec, off_own, bytes;
+    size_t off_head, off_plan, off_rec, off_own, bytes;
     long long max_units;
 };
 
@@ -217,8 +217,8 @@ bool plan_rows(const dqk_layer_desc *L, bool int2, int total_rows, int n_groups,
                          (long long)n_own * ((own_pages + kRowsPages - 1) / kRowsPages));
     P.bb = int2 ? make_layout(P.d, L->v_ch0_protect, P.d / L->group_size).bytes : b16_block_bytes(P.d);
     const size_t heads = (size_t)total_rows * L->num_q_heads;
-    P.off_scale = int2 ? round_up(heads * P.d * 2, 256) : 0;
-    P.off_plan = P.off_scale + (int2 ? round_up(heads * sizeof(float), 256) : 0);
+    P.off_head = int2 ? round_up(heads * P.d * 2, 256) : 0;
+    P.off_plan = P.off_head + (int2 ? round_up(heads * sizeof(float2), 256) : 0);
     P.off_rec = P.off_plan + round_up(rows_plan_bytes((size_t)n_groups + n_own), 256);
     const size_t row = rec_stride(P.d) * sizeof(float);
     P.off_own = P.off_rec + round_up((size_t)P.slots * 2 * kRowsHalf * row, 256);
@@ -287,8 +287,9 @@ dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost
     p.ktiles = tiles / 2;
     p.vtiles = tiles - p.ktiles;
     // page flags: at most kRowsFlags units between their copies and the softmax
-    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kRoom - 4 * T::kTile) / (kRowsPages * P.bb)) : 0;
-    const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb;
+    constexpr size_t kCh0 = T::kInt2 ? kRowsCh0 * rows_ch0_bytes(VCH0) : 0;
+    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kRoom - 4 * T::kTile - kCh0) / (kRowsPages * P.bb)) : 0;
+    const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb + kCh0;
     dqk_status st = prepare_kernel<k_rows<D, kFmt, kW, NS, VCH0>>(dev, smem, T::kThreads);
     if (st != DQK_OK) return st;
     CUtensorMap map = {};
@@ -311,20 +312,20 @@ dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost
 
 // the INT2 cache: transformed and pruned fp16 query rows first
 template <int D, int G, int RB>
-dqk_status launch_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float *scale) {
+dqk_status launch_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float2 *head) {
     const size_t smem = query_rows_smem<D, G, RB>();
     const dqk_status st = prepare_kernel<k_query_rows<D, G, RB>>(dev, smem, kQueryThreads);
     if (st != DQK_OK) return st;
     return launch_overlapped(k_query_rows<D, G, RB>, dim3((p.total_rows + RB - 1) / RB, p.hkv), kQueryThreads, smem, a.stream,
-                             a.layer->t_q, a.q, (int)a.q_dtype, p.total_rows, p.hq, a.pct, p.qs, rows, scale, a.sel_out);
+                             a.layer->t_q, a.q, (int)a.q_dtype, p.total_rows, p.hq, a.pct, p.qs, rows, head, a.sel_out);
 }
 
 template <int D, int G>
-dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float *scale) {
+dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float2 *head) {
     // four rows per staged transform once one row each makes more than three CTAs per SM: the whole decode with 1 and
     // 4 (us; 8 kv heads, 1024 shared tokens) 38 and 42 at 32 rows, 49 and 51 at 48, 63 and 59 at 64, 97 and 93 at 128
-    return (long long)p.total_rows * p.hkv > 3 * 148 ? launch_query_rows<D, G, 4>(a, p, dev, rows, scale)
-                                                     : launch_query_rows<D, G, 1>(a, p, dev, rows, scale);
+    return (long long)p.total_rows * p.hkv > 3 * 148 ? launch_query_rows<D, G, 4>(a, p, dev, rows, head)
+                                                     : launch_query_rows<D, G, 1>(a, p, dev, rows, head);
 }
 
 template <int D>
@@ -338,14 +339,14 @@ dqk_status run_rows_d(const RowsCall &a, const RowsPlanHost &P, RowsParams &p, i
     }
     char *ws = static_cast<char *>(a.ws);
     uint16_t *rows = reinterpret_cast<uint16_t *>(ws);
-    float *scale = reinterpret_cast<float *>(ws + P.off_scale);
-    const dqk_status st = P.G == 1   ? run_query_rows<D, 1>(a, p, dev, rows, scale)
-                          : P.G == 2 ? run_query_rows<D, 2>(a, p, dev, rows, scale)
-                          : P.G == 4 ? run_query_rows<D, 4>(a, p, dev, rows, scale)
-                                     : run_query_rows<D, 8>(a, p, dev, rows, scale);
+    float2 *head = reinterpret_cast<float2 *>(ws + P.off_head);
+    const dqk_status st = P.G == 1   ? run_query_rows<D, 1>(a, p, dev, rows, head)
+                          : P.G == 2 ? run_query_rows<D, 2>(a, p, dev, rows, head)
+                          : P.G == 4 ? run_query_rows<D, 4>(a, p, dev, rows, head)
+                                     : run_query_rows<D, 8>(a, p, dev, rows, head);
     if (st != DQK_OK) return st;
     p.q = rows;
-    p.q_scale = scale;
+    p.q_head = head;
     const bool one = a.layer->group_size == D, v0 = a.layer->v_ch0_protect != 0;
     if (one) return v0 ? run_rows_kernels<D, 2, 1, 1, true>(a, p, P, dev)
                        : run_rows_kernels<D, 2, 1, 1, false>(a, p, P, dev);

@@ -77,9 +77,9 @@ struct RowsParams {
     const int *own_lens, *own_table;
     int own_max_pages;
     // queries: BF16 cache, the caller's rows [total_rows][hq][D]; INT2 cache,
-    // prepared fp16 rows and their scales (k_query_rows)
+    // prepared fp16 rows, their scales and their factors of channel 0 (k_query_rows)
     const void *q;
-    const float *q_scale;
+    const float2 *q_head;
     float qs;
     struct RowsPlan *plan;      // what the merge needs of the split (written by the row kernel)
     float *rec, *own_rec;       // split records of the groups' and of the own items
@@ -457,13 +457,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// BF16 bits -> fp16, saturating at the largest finite value (channel 0 of the
-// INT2 cache; fp16 holds every BF16 mantissa exactly from 2^-14 up).
-__device__ __forceinline__ uint16_t bf16_to_f16_sat(uint32_t b) {
-    const float x = __uint_as_float(b << 16);
-    return __half_as_ushort(__float2half_rn(x > 65504.0f ? 65504.0f : x < -65504.0f ? -65504.0f : x));
-}
-
 // One packed block in a warp's registers, in the operand order of the stored
 // codes.  keys(s): key channels 16s..16s+15 of the page's 16 tokens, as four
 // 8 x 8 matrices {b0, b1 of tokens 0-7, b0, b1 of tokens 8-15}; a lane holds
@@ -471,11 +464,13 @@ __device__ __forceinline__ uint16_t bf16_to_f16_sat(uint32_t b) {
 // channels come in the order rows_channel_pos gives, and the query rows use it too.
 // values(m): value channels 16m..16m+15 (rows) by tokens, as matrices
 // {channels 0-7: tokens 0-7, 8-15; channels 8-15: tokens 0-7, 8-15}.
-template <int D, int NS, bool VCH0>
+// A protected channel 0's slot holds code 0, hence the group's finite min: the queries have a zero there, and
+// the accumulator's column is not used (rows_half has the channel).
+template <int D, int NS>
 struct PageInt2 {
     static constexpr int NG = D / 32;
-    uint32_t kw[NG], ks[2][NS], km[2][NS], k0[2];   // k0: fp16 bits of channel 0, token halves
-    uint32_t vw[NG], vh[NG], vs[2][NS], vm[2][NS], v0[2];
+    uint32_t kw[NG], ks[2][NS], km[2][NS];
+    uint32_t vw[NG], vh[NG], vs[2][NS], vm[2][NS];
     int gid, tig;
     template <int N>
     static __device__ __forceinline__ void words(uint32_t (&r)[N], uint32_t a) {
@@ -504,14 +499,11 @@ struct PageInt2 {
             }
         }
     }
-    static constexpr Layout kL = make_layout(D, VCH0 ? 1 : 0, NS);
+    static constexpr Layout kL = make_layout(D, 0, NS);   // section offsets do not depend on v_ch0 (V0 is last)
     __device__ __forceinline__ void load_keys(uint32_t blk, int lane) {
         gid = lane >> 2;
         tig = lane & 3;
         words<NG>(kw, blk + kL.kc + lane * 4 * NG);
-        const uint32_t k0w = ld_s32(blk + kL.k0 + gid * 4);
-        k0[0] = bf16_to_f16_sat(k0w & 0xffffu);
-        k0[1] = bf16_to_f16_sat(k0w >> 16);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             pairs(ks[h], blk + kL.ks + (gid + 8 * h) * 2 * NS);
@@ -526,10 +518,6 @@ struct PageInt2 {
         for (int h = 0; h < 2; ++h) {
             words<NS>(vs[h], blk + kL.vs + (tig + 4 * h) * 4 * NS);
             words<NS>(vm[h], blk + kL.vm + (tig + 4 * h) * 4 * NS);
-            if constexpr (VCH0) {
-                const uint32_t w = ld_s32(blk + kL.v0 + (tig + 4 * h) * 4);
-                v0[h] = (uint32_t)bf16_to_f16_sat(w & 0xffffu) | ((uint32_t)bf16_to_f16_sat(w >> 16) << 16);
-            }
         }
 #pragma unroll
         for (int k = 0; k < NG; ++k) vh[k] = vw[k] >> 10;
@@ -551,7 +539,6 @@ struct PageInt2 {
                 case 2: r[2 * h] = key_pair<2>(w, 0, ks[h][gs], km[h][gs]); r[2 * h + 1] = key_pair<2>(w, 1, ks[h][gs], km[h][gs]); break;
                 default: r[2 * h] = key_pair<3>(w, 0, ks[h][gs], km[h][gs]); r[2 * h + 1] = key_pair<3>(w, 1, ks[h][gs], km[h][gs]); break;
             }
-            if (s == 0 && tig == 0) r[2 * h] = (r[2 * h] & 0xffff0000u) | k0[h];
         }
     }
     template <int I>
@@ -576,12 +563,7 @@ struct PageInt2 {
 #pragma unroll
         for (int cr = 0; cr < 2; ++cr)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                r[2 * cr + h] = value(m, cr, h);
-                if constexpr (VCH0) {
-                    if (m == 0 && cr == 0 && gid == 0) r[2 * cr + h] = v0[h];
-                }
-            }
+            for (int h = 0; h < 2; ++h) r[2 * cr + h] = value(m, cr, h);
     }
 };
 
@@ -599,9 +581,14 @@ __host__ __device__ __forceinline__ int rows_channel_pos(int c) {
 // BF16 tile: page after page as one tensor copy lays it, [column block][16 token
 // rows]; the 8-row groups of a half are then a page's size apart.  INT2 tile, keys:
 // [column block][half][page][8 token rows]; values: [half][D channel rows], tokens
-// along the row.
+// along the row.  Behind the packed blocks: channel 0 of a unit's keys and (protected) of its values in fp32,
+// [unit modulo kRowsCh0][keys, values][half][page][8 tokens], 0 where no token is.
 // ---------------------------------------------------------------------------
 constexpr int kRowsMaxTiles = 8, kRowsMaxRaw = 8;
+// Units whose channel 0 is held.  A unit's is written once the key tile of two units before (INT2 has two) is free:
+// both warpgroups have then formed scores of the two units before it, so they are through with all units before those.
+constexpr int kRowsCh0 = 4;
+__host__ __device__ constexpr uint32_t rows_ch0_bytes(bool v_ch0) { return kRowsKv * 4 * (v_ch0 ? 2 : 1); }   // of a unit
 struct RowsBars {
     uint64_t full[kRowsMaxTiles], empty[kRowsMaxTiles];        // operand tiles: the ring of keys, then that of values
     uint64_t raw_full[kRowsMaxRaw], raw_empty[kRowsMaxRaw];    // packed blocks
@@ -765,14 +752,15 @@ __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtenso
     }
 }
 
-// INT2: packed blocks -> fp16 operand tiles.  Keys as rows of tokens; values as
+// INT2: packed blocks -> fp16 operand tiles, and channel 0 in fp32.  Keys as rows of tokens; values as
 // rows of channels (the order their codes are stored in), 64 tokens per 128-byte row.
 // A unit's keys come first, and on their own: their tile is free as soon as the scores of
 // two units before are formed, the values' only after that unit's weights.
 template <int D, int NS, bool VCH0>
-__device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *raw, int warp,
-                                            int lane) {
+__device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, unsigned char *tiles, unsigned char *raw,
+                                            uint32_t ch0, int warp, int lane) {
     constexpr int kTile = kRowsKv * D * 2;
+    constexpr Layout kL = make_layout(D, VCH0 ? 1 : 0, NS);
     RowsWalk s;
     RowsRing rr, rk, rv;
     int unit = 0;
@@ -791,9 +779,18 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
             const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
             const uint32_t blk = smem_addr(raw) + (uint32_t)(rs * kRowsPages * p.bb);
 #pragma unroll 1
-            for (int pg = warp; pg < pages; pg += kRowsUnpackWarps) {
-                if (!((have >> pg) & 1u)) continue;   // its scores are masked
-                PageInt2<D, NS, VCH0> b;
+            for (int pg = warp; pg < kRowsPages; pg += kRowsUnpackWarps) {
+                const bool in = (have >> pg) & 1u;
+                if (lane < kPage) {
+                    const uint32_t at = ch0 + (uint32_t)(unit & (kRowsCh0 - 1)) * rows_ch0_bytes(VCH0) +
+                                        (uint32_t)((lane >> 3) * (kRowsKv * 2) + pg * 32 + (lane & 7) * 4);
+                    const bool token = in && kPage * pg + lane < nv;
+                    st_s32(at, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.k0 + 2 * k0_idx(lane))) << 16 : 0u);
+                    if constexpr (VCH0)
+                        st_s32(at + kRowsKv * 4, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.v0 + 2 * lane)) << 16 : 0u);
+                }
+                if (!in) continue;   // its scores are masked
+                PageInt2<D, NS> b;
                 b.load_keys(blk + (uint32_t)(pg * p.bb), lane);
                 const uint32_t row = tile0 + (uint32_t)sk * kTile + ka + (uint32_t)pg * 1024;
 #pragma unroll
@@ -813,7 +810,7 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
             for (int pg = warp; pg < pages; pg += kRowsUnpackWarps) {
                 const uint32_t row = tile0 + (uint32_t)sv * kTile + va + (uint32_t)((pg ^ r8) << 4);
                 if ((have >> pg) & 1u) {
-                    PageInt2<D, NS, VCH0> b;
+                    PageInt2<D, NS> b;
                     b.load_values(blk + (uint32_t)(pg * p.bb), lane);
                     // tokens past the list's end hold stale bytes: zeros, so that they add nothing
                     const int n = nv - kPage * pg;
@@ -1039,22 +1036,54 @@ __device__ __forceinline__ void rows_pack(float2 y, uint32_t &hi, uint32_t &lo) 
     if constexpr (kW == 2) lo = pack_bf16x2(y.x - __uint_as_float(hi << 16), y.y - __uint_as_float(hi & 0xffff0000u));
 }
 
-// 16 scores of a thread's row -> weights 2^(x qs - base), packed in pairs (kW == 2: low parts 32 words on);
-// their sum is added to s0, s1 and their largest score taken into m0, m1.
-template <bool F16, int kW>
-__device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2, float2 b2, uint32_t *pk, float2 &s0, float2 &s1,
-                                             float &m0, float &m1) {
+// INT2: channel 0 of half a unit's keys (and values) in shared memory, and the row's factor of it.
+struct RowsKey0 {
+    uint32_t k0;
+    float q0;
+    __device__ __forceinline__ RowsKey0 at(int c) const { return {k0 + 64u * c, q0}; }   // 16 tokens on
+    __device__ __forceinline__ uint32_t v0() const { return k0 + kRowsKv * 4; }
+};
+
+// What the running sums of a half hold: weights, their products with value channel 0, largest score.
+struct RowsSums {
+    float2 s0, s1, z0, z1;
+    float m0, m1;
+    __device__ __forceinline__ void clear() { s0 = s1 = z0 = z1 = make_float2(0.0f, 0.0f); }
+    __device__ __forceinline__ float largest() const { return fmaxf(m0, m1); }
+};
+
+// 16 scores of a thread's row -> weights 2^(x qs - base), packed in pairs (kW == 2: low parts 32 words on), their
+// sums, and their largest: of x, or (INT2) of x qs + k_0 q_0 - base.
+template <bool F16, int kW, bool VCH0>
+__device__ __forceinline__ void rows_weights(const uint32_t (&u)[16], float2 q2, float2 b2, const RowsKey0 &ch, uint32_t *pk,
+                                             RowsSums &a) {
     float2 e[8], y[8];
+    if constexpr (F16) {
+        const float2 c2 = make_float2(ch.q0, ch.q0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = fma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), q2, b2);
+        for (int i = 0; i < 8; i += 2) {
+            const uint4 k = ld_s128(ch.k0 + 8 * i);
+            e[i] = fma2(make_float2(__uint_as_float(k.x), __uint_as_float(k.y)), c2, b2);
+            e[i + 1] = fma2(make_float2(__uint_as_float(k.z), __uint_as_float(k.w)), c2, b2);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        e[i] = fma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), q2, F16 ? e[i] : b2);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = make_float2(fast_exp2(e[i].x), fast_exp2(e[i].y));
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        m0 = max3(m0, __uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-        m1 = max3(m1, __uint_as_float(u[2 * i + 2]), __uint_as_float(u[2 * i + 3]));
-        s0 = add2(s0, y[i]);
-        s1 = add2(s1, y[i + 1]);
+        a.m0 = F16 ? max3(a.m0, e[i].x, e[i].y) : max3(a.m0, __uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        a.m1 = F16 ? max3(a.m1, e[i + 1].x, e[i + 1].y)
+                   : max3(a.m1, __uint_as_float(u[2 * i + 2]), __uint_as_float(u[2 * i + 3]));
+        if constexpr (VCH0) {
+            const uint4 v = ld_s128(ch.v0() + 8 * i);
+            a.z0 = fma2(y[i], make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), a.z0);
+            a.z1 = fma2(y[i + 1], make_float2(__uint_as_float(v.z), __uint_as_float(v.w)), a.z1);
+        }
+        a.s0 = add2(a.s0, y[i]);
+        a.s1 = add2(a.s1, y[i + 1]);
         rows_pack<F16, kW>(y[i], pk[i], pk[i + (kW - 1) * 32]);
         rows_pack<F16, kW>(y[i + 1], pk[i + 1], pk[i + 1 + (kW - 1) * 32]);
     }
@@ -1075,34 +1104,50 @@ __device__ __forceinline__ void rows_rescale(uint32_t tO, float f) {
 }
 
 // The largest score of a first half.
-__device__ __forceinline__ float rows_largest(uint32_t tS, float qs) {
+template <bool F16>
+__device__ __forceinline__ float rows_largest(uint32_t tS, float qs, const RowsKey0 &ch) {
     float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t u[16];
         tm_ld16(tS + 16 * c, u);
         tm_ready16(u);
+        if constexpr (F16) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const uint4 k = ld_s128(ch.at(c).k0 + 4 * i);
+                u[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), qs, ch.q0 * __uint_as_float(k.x)));
+                u[i + 1] = __float_as_uint(fmaf(__uint_as_float(u[i + 1]), qs, ch.q0 * __uint_as_float(k.y)));
+                u[i + 2] = __float_as_uint(fmaf(__uint_as_float(u[i + 2]), qs, ch.q0 * __uint_as_float(k.z)));
+                u[i + 3] = __float_as_uint(fmaf(__uint_as_float(u[i + 3]), qs, ch.q0 * __uint_as_float(k.w)));
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
             m0 = max3(m0, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
             m1 = max3(m1, __uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]));
         }
     }
-    return fmaxf(m0, m1) * qs;
+    return F16 ? fmaxf(m0, m1) : fmaxf(m0, m1) * qs;
 }
 
 // The weights of a thread's row for half a unit: S (64 columns at tS) becomes P~
 // (packed pairs: its first 32 columns, low parts in the others), and the reference m and the sum l of the row follow.  A half
 // whose scores pass the reference by more than the slack (rare) is taken again after the reference
-// has moved and what was summed -- l, and the accumulator, once `settled` has waited for it -- has been rescaled.
-template <int D, bool F16, int kW, typename Settled>
-__device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, float lift, float &m, float &l,
-                                          Settled settled) {
+// has moved and what was summed -- l, z, and the accumulator, once `settled` has waited for it -- has been rescaled.
+// Channel 0 of the INT2 cache does not go through fp16, which would round it below 2^-14 and cut it off at 65504: the
+// keys' is added to the scores, the products with the values' (z, protected) are summed, both in fp32.  That costs 4 %
+// (64 sequences behind 128K tokens 286 and 297 us, a chat batch 50.1 and 52.3).
+template <int D, bool F16, int kW, bool VCH0, typename Settled>
+__device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, const RowsKey0 &ch, float lift, float &m,
+                                          float &l, float &z, Settled settled) {
     uint32_t pk[32 * kW];
     const float2 q2 = make_float2(qs, qs);
     float base = (m == -INFINITY ? 0.0f : m) - lift;
-    float2 b2 = make_float2(-base, -base), s0 = make_float2(0.0f, 0.0f), s1 = s0;
-    float m0 = -INFINITY, m1 = -INFINITY;
+    float2 b2 = make_float2(-base, -base);
+    RowsSums a;
+    a.clear();
+    a.m0 = a.m1 = -INFINITY;
     // 16-column loads in registers together (INT2 has 128 registers a thread, and low parts take theirs)
     constexpr int kAtOnce = F16 || kW == 2 ? 2 : 4;
 #pragma unroll
@@ -1113,30 +1158,32 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, 
 #pragma unroll
         for (int c = 0; c < kAtOnce; ++c) tm_ready16(x[c]);
 #pragma unroll
-        for (int c = 0; c < kAtOnce; ++c) rows_weights<F16, kW>(x[c], q2, b2, pk + 8 * (c0 + c), s0, s1, m0, m1);
+        for (int c = 0; c < kAtOnce; ++c) rows_weights<F16, kW, VCH0>(x[c], q2, b2, ch.at(c0 + c), pk + 8 * (c0 + c), a);
     }
-    const float mx = fmaxf(m0, m1) * qs;
+    const float mx = F16 ? a.largest() + base : a.largest() * qs;
     const bool move = valid && mx > m + kRowsSlack;   // (lanes without a row hold anything)
     if (__any_sync(0xffffffffu, move)) {
         // the references are whole numbers: moving one scales by a power of two
         const float to = move ? ceilf(mx) : m, f = !move || m == -INFINITY ? 1.0f : fast_exp2(m - to);
         m = to;
         l *= f;
+        z *= f;
         int acc = settled();   // 1: the accumulator holds earlier halves, 0: nothing yet, -1: abort
         if (acc < 0) return false;
         if (acc) rows_rescale<D>(tO, f);
         base = (m == -INFINITY ? 0.0f : m) - lift;
         b2 = make_float2(-base, -base);
-        s0 = s1 = make_float2(0.0f, 0.0f);
+        a.clear();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t y[16];
             tm_ld16(tS + 16 * c, y);
             tm_ready16(y);
-            rows_weights<F16, kW>(y, q2, b2, pk + 8 * c, s0, s1, m0, m1);
+            rows_weights<F16, kW, VCH0>(y, q2, b2, ch.at(c), pk + 8 * c, a);
         }
     }
-    l += (s0.x + s0.y) + (s1.x + s1.y);
+    l += (a.s0.x + a.s0.y) + (a.s1.x + a.s1.y);
+    if constexpr (VCH0) z += (a.z0.x + a.z0.y) + (a.z1.x + a.z1.y);
 #pragma unroll
     for (int i = 0; i < 2 * kW; ++i) tm_st16(tS + 16 * i, pk + 16 * i);
     tm_wait_st();
@@ -1188,8 +1235,9 @@ __device__ __forceinline__ void rows_query(const RowsParams &p, const RowsPart &
 }
 
 // Softmax warpgroup w.
-template <int D, int kFmt, int kW>
-__device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, unsigned char *qmem, uint32_t tmem, int w, int cta) {
+template <int D, int kFmt, int kW, bool VCH0>
+__device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, unsigned char *qmem, uint32_t ch0, uint32_t tmem, int w,
+                                             int cta) {
     using T = RowsShape<D, kFmt>;
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16, qtile = smem_addr(qmem) + (uint32_t)(w * T::kParts * T::kTile);
@@ -1210,9 +1258,13 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
     rows_query<D, kFmt>(p, t, qtile, r);
     queries_in(t);
     while (s.live) {
-        float m = -INFINITY, l = 0.0f, qs = p.qs;
+        float m = -INFINITY, l = 0.0f, z = 0.0f, qs = p.qs, q0 = 0.0f;
         if constexpr (kFmt == 2) {
-            if (t.valid) qs = p.q_scale[t.at];
+            if (t.valid) {
+                const float2 x = p.q_head[t.at];
+                qs = x.x;
+                q0 = x.y;
+            }
         }
         const int step = s.both() ? 1 : 2;
         RowsWalk sn;          // the next segment
@@ -1239,13 +1291,16 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     rows_query<D, kFmt>(p, tn, qtile, r);
                 }
                 if (t.any) {   // warps whose 32 rows are all past the tile leave the weights as they are: rows do not mix
-                    const uint32_t have = B.flags[(unit0 + v - s.v0) & (kRowsFlags - 1)];
+                    const int unit = unit0 + v - s.v0;
+                    const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
+                    const RowsKey0 ch{kFmt == 2 ? ch0 + (uint32_t)(unit & (kRowsCh0 - 1)) * rows_ch0_bytes(VCH0) + h * (kRowsKv * 2) : 0u,
+                                     q0};
                     if (nv < kRowsKv || have != (1u << kRowsPages) - 1u) rows_mask(tS + 64 * h, nv, have, h);
                     const bool none = v == t.vf && h == 0;
-                    if (none) m = ceilf(rows_largest(tS, qs));   // no reference yet
+                    if (none) m = ceilf(rows_largest<kFmt == 2>(tS, qs, ch));   // no reference yet
                     // the half before this one may still be on its way into the accumulator (the one before that is not:
                     // these scores lie where its weights were)
-                    ok = rows_half<D, kFmt == 2, kW>(tS + 64 * h, tO, t.valid, qs, T::kLift, m, l, [&]() {
+                    ok = rows_half<D, kFmt == 2, kW, VCH0>(tS + 64 * h, tO, t.valid, qs, ch, T::kLift, m, l, z, [&]() {
                         if (none) return 0;
                         if (!__all_sync(0xffffffffu, rows_wait(&B.o_step[w], (pn - 1) & 1u, B, p.wait_ns))) return -1;
                         tm_fence_after();
@@ -1301,6 +1356,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     uint32_t o[16];
                     tm_ld16(tO + 16 * c, o);
                     tm_ready16(o);
+                    if (VCH0 && c == 0) o[0] = __float_as_uint(z);
                     if (t.valid) {
                         float y[16];
 #pragma unroll
@@ -1342,6 +1398,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                     uint32_t o[16];
                     tm_ld16(tO + 16 * c, o);
                     tm_ready16(o);
+                    if (VCH0 && c == 0) o[0] = __float_as_uint(z);
                     if (t.valid) {
                         float4 *dst = reinterpret_cast<float4 *>(rec + kRecHead + 16 * c);
 #pragma unroll
@@ -1383,6 +1440,7 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     unsigned char *tiles = rows_smem + ((1024u - (smem_addr(rows_smem) & 1023u)) & 1023u);
     unsigned char *qmem = tiles + (size_t)(p.ktiles + p.vtiles) * T::kTile;
     unsigned char *raw = qmem + 2 * T::kParts * T::kTile;
+    const uint32_t ch0 = T::kInt2 ? smem_addr(raw) + (uint32_t)(p.raw_stages * kRowsPages * p.bb) : 0u;
     __shared__ RowsBars B;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
@@ -1425,7 +1483,7 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     tm_fence_after();
     const uint32_t tmem = B.tmem;
     if (warp < 8) {
-        rows_softmax<D, kFmt, kW>(p, B, qmem, tmem, warp >> 2, blockIdx.x);
+        rows_softmax<D, kFmt, kW, VCH0>(p, B, qmem, ch0, tmem, warp >> 2, blockIdx.x);
     } else {
         if (warp == 8) rows_producer<D, kFmt>(p, &map, B, tiles, raw, lane);
         else if (warp < 11) {
@@ -1434,7 +1492,7 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
         } else if constexpr (!T::kInt2) {
             rows_tails<D>(p, B, tiles, lane);
         } else {
-            if (warp >= 12) rows_unpack<D, NS, VCH0>(p, B, tiles, raw, warp - 12, lane);
+            if (warp >= 12) rows_unpack<D, NS, VCH0>(p, B, tiles, raw, ch0, warp - 12, lane);
         }
     }
     grid_dependents_launch();

@@ -375,7 +375,9 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
  * dqk_decode, with the same kept channels; T_Q 16-byte aligned.  Scores and
  * values use fp16 operands (queries scaled per row, 2^-11 per kept channel;
  * k^ and v^ rounded once, 2^-11; weights 2^-11) with fp32 accumulation:
- * dequantized magnitudes above fp16's 65504 are outside its range.
+ * dequantized magnitudes above fp16's 65504 are outside its range.  Channel 0 of
+ * the keys and a protected channel 0 of the values are BF16 in the cache and
+ * enter in fp32, whatever their magnitude.
  * dqk_bf16_prefix_decode (BF16 cache): fp32 queries are carried as BF16 high +
  * low parts, accumulation in fp32.  With an fp32 `out` so are the softmax weights
  * (2^-16, as in dqk_bf16_decode); with a BF16 `out`, whose own rounding is 2^-8,
