@@ -312,7 +312,8 @@ struct RowsPlan {
 };
 __host__ __device__ constexpr size_t rows_plan_bytes(size_t lists) { return sizeof(RowsPlan) + 16 * lists; }
 
-// By one warp of the grid's first CTA.
+// By one warp of the grid's first CTA, which also reports starts that run backwards (their groups are taken as
+// empty, and others may overlap).
 __device__ __forceinline__ void rows_write_plan(const RowsParams &p, int lane) {
     const int n = p.n_groups + p.n_own;
     long long base = 0, tbase = 0;
@@ -320,6 +321,7 @@ __device__ __forceinline__ void rows_write_plan(const RowsParams &p, int lane) {
         const int i = i0 + lane;
         RowsList r{0, 1, 0, 0};
         if (i < n) r = rows_list(p, i);
+        if (i < p.n_groups && p.row_start[i + 1] < p.row_start[i]) dqk_flag_error(kErrBounds);
         const int t = i < p.n_groups ? r.tiles : 0;
         const long long ui = warp_scan(r.units, lane), ti = warp_scan(t, lane);
         if (i < n) {

@@ -369,7 +369,8 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
  *  workspace        (device) at least the workspace size, 256-byte aligned;
  *                   scratch, no initialisation.
  * Lengths beyond a page table's reach are cut to it, bad page ids skipped, and
- * both set the device error word.
+ * both set the device error word; so do starts that run backwards, with which
+ * `out` is undefined.  Starts outside 0..batch are cut to it.
  *
  * dqk_prefix_decode (INT2 cache): T_Q, sparsity_pct and sel_out as in
  * dqk_decode, with the same kept channels; T_Q 16-byte aligned.  Scores and
