@@ -194,8 +194,8 @@ namespace {
 // sections 256-byte aligned.
 struct RowsPlanHost {
     int d, G, bb;
-    bool slot_pairs;
-    long long slots, own_slots, tiles;
+    bool rec_pairs;
+    long long rec_step;
     size_t off_head, off_plan, off_rec, off_own, bytes;
     long long max_units;
 };
@@ -208,21 +208,23 @@ bool plan_rows(const dqk_layer_desc *L, bool int2, int total_rows, int n_groups,
     if ((long long)total_rows * L->num_q_heads >= (1LL << 31) / 2) return false;
     if (((long long)max_pages + own_pages) * kPage >= (1LL << 31)) return false;
     if (L->num_pages * hkv >= (1LL << 31)) return false;   // block numbers are tensor-copy coordinates
-    P.tiles = n_groups + (long long)total_rows * P.G / kRowsTile;   // >= the groups' row tiles
-    if (P.tiles * hkv >= (1LL << 31) / 2 || (long long)n_own * hkv >= (1LL << 31) / 2) return false;
-    P.slot_pairs = !n_own && P.tiles * hkv > kRowsMaxCtas;   // rows_slot
-    P.slots = P.slot_pairs ? 2 * kRowsMaxCtas : kRowsMaxCtas + P.tiles * hkv;
-    P.own_slots = n_own ? kRowsMaxCtas + n_own * hkv : 0;
-    P.max_units = hkv * (2 * P.tiles * ((max_pages + kRowsPages - 1) / kRowsPages) +
+    const long long tiles = n_groups + (long long)total_rows * P.G / kRowsTile;   // >= the groups' row tiles
+    if (tiles * hkv >= (1LL << 31) / 2 || (long long)n_own * hkv >= (1LL << 31) / 2) return false;
+    P.max_units = hkv * (2 * tiles * ((max_pages + kRowsPages - 1) / kRowsPages) +
                          (long long)n_own * ((own_pages + kRowsPages - 1) / kRowsPages));
+    // records (rows_record): both forms grow with every size, hence so does the smaller one
+    const long long ctas = std::min<long long>(kRowsMaxCtas, P.max_units);
+    P.rec_step = 2 * std::min<long long>(kRowsHalf, (long long)total_rows * P.G);
+    const long long by_item = ctas * P.rec_step + 2 * (long long)total_rows * L->num_q_heads, by_cta = 2 * ctas * P.rec_step;
+    P.rec_pairs = !n_own && by_cta < by_item;
     P.bb = int2 ? make_layout(P.d, L->v_ch0_protect, P.d / L->group_size).bytes : b16_block_bytes(P.d);
     const size_t heads = (size_t)total_rows * L->num_q_heads;
     P.off_head = int2 ? round_up(heads * P.d * 2, 256) : 0;
     P.off_plan = P.off_head + (int2 ? round_up(heads * sizeof(float2), 256) : 0);
     P.off_rec = P.off_plan + round_up(rows_plan_bytes((size_t)n_groups + n_own), 256);
     const size_t row = rec_stride(P.d) * sizeof(float);
-    P.off_own = P.off_rec + round_up((size_t)P.slots * 2 * kRowsHalf * row, 256);
-    P.bytes = P.off_own + round_up((size_t)P.own_slots * 2 * P.G * row, 256);
+    P.off_own = P.off_rec + round_up((size_t)(P.rec_pairs ? by_cta : by_item) * row, 256);
+    P.bytes = P.off_own + round_up((size_t)(n_own ? ctas + n_own * hkv : 0) * 2 * P.G * row, 256);
     return true;
 }
 
@@ -386,9 +388,9 @@ dqk_status run_rows(const RowsCall &a) {
     p.plan = reinterpret_cast<RowsPlan *>(ws + P.off_plan);
     p.rec = reinterpret_cast<float *>(ws + P.off_rec);
     p.own_rec = reinterpret_cast<float *>(ws + P.off_own);
-    p.slot_pairs = P.slot_pairs;
+    p.rec_pairs = P.rec_pairs;
+    p.rec_step = (uint32_t)P.rec_step;
     p.zero_rest = a.zero_rest;
-    p.rec_slots = P.slots;
     p.out = a.out;
     p.out_dtype = (int)a.out_dtype;
     p.hq = L->num_q_heads;

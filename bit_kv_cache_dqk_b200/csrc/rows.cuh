@@ -83,9 +83,9 @@ struct RowsParams {
     float qs;
     struct RowsPlan *plan;      // what the merge needs of the split (written by the row kernel)
     float *rec, *own_rec;       // split records of the groups' and of the own items
-    bool slot_pairs;            // see rows_slot
+    bool rec_pairs;             // see rows_record
+    uint32_t rec_step;
     bool zero_rest;             // rows of no group become zeros
-    long long rec_slots;        // slots `rec` holds (row_start out of order could ask for more)
     void *out;
     int out_dtype;
     int head;                   // cost of an item besides its units
@@ -148,27 +148,19 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
     return x;
 }
 
-// Cost and row tiles of the lists before list n; warp-collective.
-__device__ __forceinline__ void rows_sums(const RowsParams &p, int n, int lane, long long &units, long long &tiles) {
-    long long u = 0, t = 0;
-    for (int i = lane; i < n; i += 32) {
-        const RowsList r = rows_list(p, i);
-        u += r.units;
-        t += i < p.n_groups ? r.tiles : 0;
-    }
+// Cost of the lists before list n; warp-collective.
+__device__ __forceinline__ long long rows_sum(const RowsParams &p, int n, int lane) {
+    long long u = 0;
+    for (int i = lane; i < n; i += 32) u += rows_list(p, i).units;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        u += __shfl_xor_sync(0xffffffffu, u, o);
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
-    units = u;
-    tiles = t;
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
 }
 
 // The start of a CTA's walk: its range of cost [u0, u1) -- a unit is its own if it begins there --, the item
-// that holds u0 (whose first unit begins at `start`), and the row tiles of the groups before its list.
+// that holds u0 (whose first unit begins at `start`).
 struct RowsCursor {
-    long long u0, u1, start, tile0;
+    long long u0, u1, start;
     int list, mt, j;
 };
 
@@ -181,16 +173,14 @@ __device__ __forceinline__ long long rows_share(long long U, int ctas) { return 
 // The CTA's cursor at its first list; warp-collective.
 __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, int lane) {
     const int n = p.n_groups + p.n_own;
-    // one pass when every list has a lane, else the sums first
-    long long U = 0, tiles = 0, base = 0, tbase = 0;
-    if (n > 32) rows_sums(p, n, lane, U, tiles);
-    RowsCursor c{0, 0, 0, 0, n, 0, 0};
+    // one pass when every list has a lane, else the sum first
+    long long U = n > 32 ? rows_sum(p, n, lane) : 0, base = 0;
+    RowsCursor c{0, 0, 0, n, 0, 0};
     for (int i0 = 0; i0 < n; i0 += 32) {
         const int i = i0 + lane;
         RowsList r{0, 1, 0, 0};
         if (i < n) r = rows_list(p, i);
         const long long ui = warp_scan(r.units, lane);
-        const int ti = (int)warp_scan(i < p.n_groups ? r.tiles : 0, lane);
         if (n <= 32) U = __shfl_sync(0xffffffffu, ui, 31);
         if (i0 == 0) {
             const long long q = rows_share(U, p.num_ctas);
@@ -215,13 +205,11 @@ __device__ __forceinline__ RowsCursor rows_cursor(const RowsParams &p, int cta, 
             const int src = __ffs(m) - 1;
             c.list = i0 + src;
             c.start = __shfl_sync(0xffffffffu, start, src);
-            c.tile0 = tbase + __shfl_sync(0xffffffffu, ti - (i < p.n_groups ? r.tiles : 0), src);
             c.mt = __shfl_sync(0xffffffffu, mt, src);
             c.j = __shfl_sync(0xffffffffu, j, src);
             break;
         }
         base += __shfl_sync(0xffffffffu, ui, 31);
-        tbase += __shfl_sync(0xffffffffu, ti, 31);
     }
     return c;
 }
@@ -234,7 +222,7 @@ __device__ __forceinline__ int rows_begun(long long x, int w, int per) {
 
 // Walks the segments -- stretches [v0, v1) of one item's units -- of a CTA in order.
 struct RowsWalk {
-    long long start, u1, tile0;     // where the item's first unit begins, the CTA's end, row tiles of the groups before
+    long long start, u1;            // where the item's first unit begins, the CTA's end
     int list, tiles, last, per, len, row0, heads;   // the list: shape, tokens, first query row, row heads
     int mt, j, w;                   // the item: row tile, kv head, cost of a unit
     int v0, v1;
@@ -261,7 +249,6 @@ struct RowsWalk {
         load(p);
         start = c.start;
         u1 = c.u1;
-        tile0 = c.tile0;
         mt = c.mt;
         j = c.j;
         w = mt < tiles - 1 ? kRowsBothCost : last;
@@ -275,7 +262,6 @@ struct RowsWalk {
             j = 0;
             if (++mt == tiles) {
                 do {
-                    if (list < p.n_groups) tile0 += tiles;
                     if (++list >= p.n_groups + p.n_own) {
                         live = false;
                         return;
@@ -295,57 +281,57 @@ struct RowsWalk {
     __device__ __forceinline__ int units() const { return v1 - v0; }
     __device__ __forceinline__ int jobs() const { return both() ? 2 * units() : units(); }
     __device__ __forceinline__ int rows() const { return min(kRowsTile, heads - mt * kRowsTile); }
-    // record slot: CTA + item
-    __device__ __forceinline__ long long item(const RowsParams &p) const {
-        return own(p) ? (long long)row0 * p.hkv + j : (tile0 + mt) * p.hkv + j;
-    }
 };
 
 // What the row kernel leaves for the merge: cost per CTA, where each CTA's walk starts (without own
-// lists), or where each list's cost begins and the row tiles before it (with).
+// lists), or where each list's cost begins (with).
 struct RowsPlan {
     long long q;
     RowsCursor cursor[kRowsMaxCtas];
-    struct {
-        long long first, tile0;
-    } list[1];   // n_groups + n_own of them
+    long long first[1];   // n_groups + n_own of them
 };
-__host__ __device__ constexpr size_t rows_plan_bytes(size_t lists) { return sizeof(RowsPlan) + 16 * lists; }
+__host__ __device__ constexpr size_t rows_plan_bytes(size_t lists) { return sizeof(RowsPlan) + sizeof(long long) * lists; }
 
 // By one warp of the grid's first CTA, which also reports starts that run backwards (their groups are taken as
 // empty, and others may overlap).
 __device__ __forceinline__ void rows_write_plan(const RowsParams &p, int lane) {
     const int n = p.n_groups + p.n_own;
-    long long base = 0, tbase = 0;
+    long long base = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
         const int i = i0 + lane;
         RowsList r{0, 1, 0, 0};
         if (i < n) r = rows_list(p, i);
         if (i < p.n_groups && p.row_start[i + 1] < p.row_start[i]) dqk_flag_error(kErrBounds);
-        const int t = i < p.n_groups ? r.tiles : 0;
-        const long long ui = warp_scan(r.units, lane), ti = warp_scan(t, lane);
-        if (i < n) {
-            p.plan->list[i].first = base + ui - r.units;
-            p.plan->list[i].tile0 = tbase + ti - t;
-        }
+        const long long ui = warp_scan(r.units, lane);
+        if (i < n) p.plan->first[i] = base + ui - r.units;
         base += __shfl_sync(0xffffffffu, ui, 31);
-        tbase += __shfl_sync(0xffffffffu, ti, 31);
     }
     if (lane == 0) p.plan->q = rows_share(base, p.num_ctas);
 }
 
-// Record slots of the groups' items.  With own lists every segment is joined with another:
-// slot CTA + item (a CTA's segments are of consecutive items).  Without, only items that cross
-// a CTA's border are: the same, or, where there are more items than CTAs (slot_pairs), slot 2 CTA
-// for the part of an item that began in an earlier CTA, 2 CTA + 1 for one that begins here.
-__device__ __forceinline__ long long rows_slot(const RowsParams &p, long long cta, long long item, bool begins) {
-    return p.slot_pairs ? 2 * cta + (begins ? 1 : 0) : cta + item;
+// Records of the groups' segments.  An item of n row heads has n records a segment (both warpgroups take its
+// units) or, with n <= 128, two of each row head (the units go to one and the other); a segment never has more than
+// step = 2 min(128, all row heads of a kv head).  With own lists every segment is joined with another: a CTA's segments
+// are of consecutive items, so those of an item begin at CTA step + 2 (row heads of the items before), and reach no
+// further than the next one's -- of the same CTA and the next item, or of the next CTA and the same item.
+// Without, only items that cross a CTA's border are joined: the same, or, where it takes less room (rec_pairs), two
+// places of `step` records a CTA, for the part of an item that began in an earlier CTA and for one that begins here.
+// Starts that run backwards leave all of this inside the workspace, since row heads stay below those of the call.
+// (There are less than 2^30 row heads, so record numbers fit in 32 bits.)
+__device__ __forceinline__ uint32_t rows_record(const RowsParams &p, int cta, uint32_t before, bool begins) {
+    return p.rec_pairs ? (uint32_t)(2 * cta + (begins ? 1 : 0)) * p.rec_step : (uint32_t)cta * p.rec_step + 2 * before;
 }
-// Record row: warpgroup g's row r of a slot.
-__device__ __forceinline__ size_t rows_rec(long long slot, int g, int r) { return ((size_t)slot * 2 + g) * kRowsHalf + r; }
-__device__ __forceinline__ size_t rows_own_rec(long long slot, int g, int G, int r) {
-    return ((size_t)slot * 2 + g) * G + r;
+// Row heads before those of an item: of its tile of `rows` row heads from `first` of its list, kv head j.
+__device__ __forceinline__ uint32_t rows_heads_before(const RowsParams &p, int row0, int first, int rows, int j) {
+    return (uint32_t)(row0 * p.G + first) * p.hkv + (uint32_t)(j * rows);
 }
+// A record's place in its segment: row head x of a tile that both warpgroups take, or warpgroup g's of row head x.
+__device__ __forceinline__ uint32_t rows_place(bool both, int x, int g) { return (uint32_t)(both ? x : 2 * x + g); }
+// Own lists: CTA + item, two records of each of the G row heads.
+__device__ __forceinline__ uint32_t rows_own_record(const RowsParams &p, int cta, int row, int j, int x, int g) {
+    return (uint32_t)(cta + row * p.hkv + j) * 2 * p.G + rows_place(false, x, g);
+}
+__device__ __forceinline__ float *rows_at(float *rec, uint32_t record, int D) { return rec + (size_t)record * rec_stride(D); }
 
 // ---------------------------------------------------------------------------
 // tcgen05, TMEM and tensor copies
@@ -1327,18 +1313,22 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
         // a list that is whole in this segment (and has nothing to be joined with) becomes outputs here; where
         // its units went to both warpgroups in turn, the second hands its record to the first
         const bool whole = p.n_own == 0 && s.v0 == 0 && s.v1 == s.per;
-        const long long item = s.item(p), slot = rows_slot(p, cta, item, s.v0 == 0);
-        const bool fits = s.own(p) || slot < p.rec_slots, split = !s.both() && s.per > 1, joint = whole && split && fits;
+        const bool split = !s.both() && s.per > 1, joint = whole && split;
+        auto record = [&](uint32_t place) {   // of a group's segment
+            const uint32_t before = rows_heads_before(p, s.row0, s.mt * kRowsTile, s.rows(), s.j);
+            return rows_at(p.rec, rows_record(p, cta, before, s.v0 == 0) + place, D);
+        };
         if (w == 1 && pending && (joint || !whole)) {   // the first warpgroup has read the record before it is written again
             ok = __all_sync(0xffffffffu, rows_wait(&B.read, rn & 1, B, p.wait_ns));
             ++rn;
             if (!ok) return;
             pending = false;
         }
-        if (whole && (!split || (fits && w == 0))) {
+        if (whole && (!split || w == 0)) {
             float f = 1.0f, f1 = 0.0f;
-            const float *other = p.rec + rows_rec(slot, 1, r) * rec_stride(D);
+            const float *other = nullptr;
             if (joint) {
+                other = record(rows_place(false, r, 1));
                 ok = __all_sync(0xffffffffu, rows_wait(&B.join, jn & 1, B, p.wait_ns));
                 ++jn;
                 if (!ok) return;
@@ -1390,9 +1380,9 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             }
             __syncwarp();
             if (joint && lane == 0) mbar_arrive(&B.read);
-        } else if (fits) {
-            float *rec = (s.own(p) ? p.own_rec + rows_own_rec(cta + item, w, p.G, r) * rec_stride(D)
-                                   : p.rec + rows_rec(slot, w, r) * rec_stride(D));
+        } else {
+            float *rec = s.own(p) ? rows_at(p.own_rec, rows_own_record(p, cta, s.row0, s.j, r, w), D)
+                                  : record(rows_place(s.both(), s.both() ? kRowsHalf * w + r : r, w));
             if (t.valid) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);   // no unit of this segment: (-inf, 0) alone
             if (t.any && t.mine) {
 #pragma unroll 2
@@ -1416,8 +1406,6 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
                 if (lane == 0) mbar_arrive(&B.join);
                 pending = true;
             }
-        } else if (r == 0) {   // groups that overlap
-            dqk_flag_error(kErrBounds);
         }
         __syncwarp();
         tm_fence_before();   // the accumulator has been read before the next segment's first product
@@ -1540,10 +1528,10 @@ struct RowsMerge {
 #pragma unroll
         for (int e = 0; e < V; ++e) O[e] = none ? O[e] : fmaf(f, o[e], O[e]);
     }
-    // The records of row r (of warpgroup r / 128 of a two-half tile) of an item whose first unit begins
-    // at `start`: CTAs cf .. cl, both warpgroups' where the units went to one and the other.
+    // The records of row head r of an item whose first unit begins at `start`: CTAs cf .. cl, both
+    // warpgroups' where the units went to one and the other.  before: rows_heads_before of the item, or (own) its query row.
     __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, bool both, long long q,
-                                         long long item, int r, int lane) {
+                                         uint32_t before, int j, int r, int lane) {
         if (per <= 0) return;
         const int w = both ? kRowsBothCost : kRowsOneCost, shares = both ? 1 : 2;
         const int cf = (int)rows_div(start, q), cl = (int)rows_div(start + (long long)(per - 1) * w, q), n = (cl - cf + 1) * shares;
@@ -1553,18 +1541,16 @@ struct RowsMerge {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k;
-                const long long c = cf + i / shares;
+                const int c = cf + i / shares;
                 m[k] = -INFINITY;
                 l[k] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[k][e] = 0.0f;
                 // (no unit need begin in a short range)
                 const bool has = rows_begun(c * q - start, w, per) < rows_begun((c + 1) * q - start, w, per);
-                const long long slot = rows_slot(p, c, item, c == cf);
-                if (i < n && has && (own || slot < p.rec_slots)) {
-                    const int g = both ? r >> 7 : i & 1, rr = both ? r & 127 : r;
-                    load(own ? p.own_rec + rows_own_rec(c + item, g, p.G, rr) * rec_stride(D)
-                             : p.rec + rows_rec(slot, g, rr) * rec_stride(D),
+                if (i < n && has) {
+                    load(own ? rows_at(p.own_rec, rows_own_record(p, c, (int)before, j, r, i & 1), D)
+                             : rows_at(p.rec, rows_record(p, c, before, c == cf) + rows_place(both, r, i & 1), D),
                          lane, m[k], l[k], o[k]);
                 }
             }
@@ -1603,7 +1589,7 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
     if (h >= p.hq) return;
     const int j = h / p.G, hh = h - j * p.G;
     grid_dependency_wait();
-    const long long q = p.plan->q, own_first = p.plan->list[p.n_groups + row].first;
+    const long long q = p.plan->q, own_first = p.plan->first[p.n_groups + row];
     const int per = rows_list(p, p.n_groups + row).per;
     int g = -1;   // the group of the row
     for (int i0 = 0; i0 < p.n_groups && g < 0; i0 += 32) {
@@ -1615,13 +1601,14 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
     RowsMerge<D> acc;
     if (g >= 0) {
         const RowsList r = rows_list(p, g);
-        const long long first = p.plan->list[g].first, tile0 = p.plan->list[g].tile0;
-        const int rr = (row - rows_first(p, g)) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? kRowsBothCost : r.last;
+        const long long first = p.plan->first[g];
+        const int row0 = rows_first(p, g), heads = (rows_first(p, g + 1) - row0) * p.G;
+        const int rr = (row - row0) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? kRowsBothCost : r.last;
         acc.take(p, false, first + (long long)mt * p.hkv * rows_cost(p, r.per, kRowsBothCost) + j * rows_cost(p, r.per, w) + p.head,
-                 r.per, w == kRowsBothCost, q,
-                 (tile0 + mt) * p.hkv + j, rr - mt * kRowsTile, lane);
+                 r.per, w == kRowsBothCost, q, rows_heads_before(p, row0, mt * kRowsTile, min(kRowsTile, heads - mt * kRowsTile), j), j,
+                 rr - mt * kRowsTile, lane);
     }
-    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, false, q, (long long)row * p.hkv + j, hh, lane);
+    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, false, q, row, j, hh, lane);
     acc.store(p, (size_t)row * p.hq + h, lane);
 }
 
@@ -1658,7 +1645,13 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     if (x0 >= heads) return;
     RowsMerge<D> acc[kRowsMergeHeads];
     const bool both = w == kRowsBothCost;
-    const long long item = (c.tile0 + c.mt) * p.hkv + c.j;
+    // records in CTA b, in the next one and, from there, in CTA after CTA; the row heads' places in each
+    const uint32_t before = rows_heads_before(p, first, c.mt * kRowsTile, heads, c.j);
+    const uint32_t here = rows_record(p, b, before, true), next = rows_record(p, b + 1, before, false);
+    const uint32_t step_cta = p.rec_pairs ? 2 * p.rec_step : p.rec_step;
+    uint32_t place[kRowsMergeHeads];
+#pragma unroll
+    for (int k = 0; k < kRowsMergeHeads; ++k) place[k] = rows_place(both, min(x0 + k * step, heads - 1), 0);
     const int cl = (int)rows_div(c.start + (long long)(r.per - 1) * w, q);
     const int shares = both ? 1 : 2, n = (cl - b + 1) * shares;
     for (int i0 = 0; i0 < n; i0 += 2) {   // two records of every row head at a time
@@ -1666,17 +1659,12 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
         bool has[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int a = b + (i0 + e) / shares, g = (i0 + e) % shares;
-            const long long slot = rows_slot(p, a, item, a == b);
-            has[e] = i0 + e < n && slot < p.rec_slots &&
-                     rows_begun(a * q - c.start, w, r.per) < rows_begun((a + 1) * q - c.start, w, r.per);
-            if (!has[e]) continue;
+            const int a = min(b + (i0 + e) / shares, cl), g = (i0 + e) % shares;
+            has[e] = i0 + e < n && rows_begun(a * q - c.start, w, r.per) < rows_begun((a + 1) * q - c.start, w, r.per);
 #pragma unroll
-            for (int k = 0; k < kRowsMergeHeads; ++k) {
-                const int x = min(x0 + k * step, heads - 1);
-                RowsMerge<D>::load(p.rec + (both ? rows_rec(slot, x >> 7, x & 127) : rows_rec(slot, g, x)) * rec_stride(D), lane,
-                                   m[e][k], l[e][k], o[e][k]);
-            }
+            for (int k = 0; k < kRowsMergeHeads; ++k)   // (a record that was not written is inside the workspace too)
+                RowsMerge<D>::load(rows_at(p.rec, (a == b ? here : next + (uint32_t)(a - b - 1) * step_cta) + place[k] + g, D), lane, m[e][k],
+                                   l[e][k], o[e][k]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

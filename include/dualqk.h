@@ -367,7 +367,10 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
  *  out              (device) [batch][Hq][d] in out_dtype, 16-byte aligned; 0
  *                   for a sequence without any token.
  *  workspace        (device) at least the workspace size, 256-byte aligned;
- *                   scratch, no initialisation.
+ *                   scratch, no initialisation.  It grows with every argument
+ *                   of the size call: about 1 KB per row and query head (2 KB
+ *                   with own tokens) at d = 128, and up to 22 MB besides (1.4 MB
+ *                   for one sequence of 32 heads).
  * Lengths beyond a page table's reach are cut to it, bad page ids skipped, and
  * both set the device error word; so do starts that run backwards, with which
  * `out` is undefined.  Starts outside 0..batch are cut to it.
