@@ -172,7 +172,6 @@ struct DecodeArgs {
 };
 
 constexpr unsigned long long kGridWaitNs = kWaitLimitNs;
-constexpr unsigned long long kStallWaitNs = 1000000ull;     // 1 ms
 
 dqk_status check_decode(const DecodeArgs &a, DecodePlan &P, int &dev) {
     dqk_status st = check_layer(a.L);

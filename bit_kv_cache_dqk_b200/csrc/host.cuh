@@ -88,6 +88,7 @@ dqk_status prepare_kernel(int dev, size_t smem, int threads) {
 }
 
 constexpr unsigned long long kRingWaitNs = kWaitLimitNs;   // 1 s
+constexpr unsigned long long kStallWaitNs = 1000000ull;    // 1 ms: the test-only stalls
 
 // Launch with programmatic stream serialization: the kernel may start while the
 // previous one finishes, and waits for it (griddepcontrol.wait) before reading anything.

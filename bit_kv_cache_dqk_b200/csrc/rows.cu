@@ -276,6 +276,7 @@ struct RowsCall {
     size_t ws_bytes;
     cudaStream_t stream;
     bool zero_rest;                       // rows of no group: zeros, or left as they were
+    bool stall = false;                   // test only
 };
 
 template <int D, int kFmt, int kW, int NS, bool VCH0>
@@ -399,7 +400,8 @@ dqk_status run_rows(const RowsCall &a) {
     p.head = a.int2 ? kRowsHeadInt2 : kRowsHeadBf16;
     p.bb = P.bb;
     p.num_ctas = (int)std::max<long long>(1, std::min<long long>(std::min(sms, kRowsMaxCtas), P.max_units));
-    p.wait_ns = kRingWaitNs;
+    p.wait_ns = a.stall ? kStallWaitNs : kRingWaitNs;
+    p.stall = a.stall;
     return P.d == 128 ? run_rows_d<128>(a, P, p, dev) : run_rows_d<64>(a, P, p, dev);
 }
 
@@ -461,6 +463,22 @@ dqk_status dqk_bf16_prefix_decode(const dqk_layer_desc *layer, const void *q, dq
     return run_rows(RowsCall{layer, false, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
                              max_prefix_pages, max_pages ? batch : 0, seq_lens, page_table, max_pages, 0, out, out_dtype,
                              nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream), true});
+}
+
+dqk_status dqk_test_prefix_stall(const dqk_layer_desc *layer, int bf16, const void *q, dqk_dtype q_dtype, int batch,
+                                 int n_prefixes, const int *prefix_start, const int *prefix_lens, const int *prefix_table,
+                                 int max_prefix_pages, const int *seq_lens, const int *page_table, int max_pages,
+                                 int sparsity_pct, void *out, dqk_dtype out_dtype, int16_t *sel_out, void *workspace,
+                                 size_t workspace_bytes, dqk_stream_t stream) {
+    dqk_status st = bf16 ? check_layer_b16(layer) : check_layer(layer);
+    if (st != DQK_OK) return st;
+    if (!bf16 && (!layer->t_q || !aligned(layer->t_q, 16) || sparsity_pct < 0 || sparsity_pct > 99)) return DQK_ERR_INVALID_ARG;
+    st = check_prefix(batch, n_prefixes, max_prefix_pages, seq_lens, page_table, max_pages);
+    if (st != DQK_OK) return st;
+    return run_rows(RowsCall{layer, !bf16, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
+                             max_prefix_pages, max_pages ? batch : 0, seq_lens, page_table, max_pages, bf16 ? 0 : sparsity_pct,
+                             out, out_dtype, bf16 ? nullptr : sel_out, workspace, workspace_bytes,
+                             static_cast<cudaStream_t>(stream), true, true});
 }
 
 dqk_status dqk_bf16_cross_attention(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch, int total_q,

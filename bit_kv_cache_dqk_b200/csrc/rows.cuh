@@ -91,6 +91,7 @@ struct RowsParams {
     int head;                   // cost of an item besides its units
     int hq, hkv, G, bb, ktiles, vtiles, raw_stages, num_ctas;
     unsigned long long wait_ns;
+    bool stall;                 // test only: CTA 0's producer never fills the stage of its second unit
 };
 
 // Tokens of a list, cut to what its page table can hold.
@@ -691,6 +692,7 @@ __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtenso
             const bool have = in && phys >= 0 && phys < p.num_pages;
             const int blk = have ? phys * p.hkv + s.j : 0;
             if (in && !have && h == 0) dqk_flag_error(kErrBounds);
+            const bool fill = !(p.stall && blockIdx.x == 0 && unit == 1);
             page += kRowsPages;
             phys = page < npages ? tab[page] : -1;   // the next unit's, on its way while this one waits
             const uint32_t m = __ballot_sync(0xffffffffu, have) & ((1u << kRowsPages) - 1u);
@@ -700,10 +702,10 @@ __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtenso
                 if (!ok) break;
                 if (lane == 0) {
                     B.flags[unit & (kRowsFlags - 1)] = m;
-                    mbar_arrive_expect_tx(&B.raw_full[ring[0].st], nb * (uint32_t)p.bb);
+                    if (fill) mbar_arrive_expect_tx(&B.raw_full[ring[0].st], nb * (uint32_t)p.bb);
                 }
                 __syncwarp();
-                if (h == 0 && have)
+                if (h == 0 && have && fill)
                     bulk_copy_g2s(raw + ((size_t)ring[0].st * kRowsPages + pg) * p.bb, p.pool + (size_t)blk * p.bb, (uint32_t)p.bb,
                                   &B.raw_full[ring[0].st]);
                 ring[0].next(p.raw_stages);
@@ -715,10 +717,10 @@ __device__ __forceinline__ void rows_producer(const RowsParams &p, const CUtenso
                     if (!ok) break;
                     if (lane == 0) {
                         if (kv == 0) B.flags[unit & (kRowsFlags - 1)] = m;
-                        mbar_arrive_expect_tx(&B.full[st], nb * (uint32_t)T::kPageBytes);
+                        if (fill) mbar_arrive_expect_tx(&B.full[st], nb * (uint32_t)T::kPageBytes);
                     }
                     __syncwarp();
-                    if (h == 0 && have)
+                    if (h == 0 && have && fill)
                         tensor_copy(tiles + (size_t)st * T::kTile + pg * T::kPageBytes, map, kv * kPage, blk, &B.full[st]);
                     ring[kv].next(kv ? p.vtiles : p.ktiles);
                 }
@@ -1474,6 +1476,7 @@ __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     const uint32_t tmem = B.tmem;
     if (warp < 8) {
         rows_softmax<D, kFmt, kW, VCH0>(p, B, qmem, ch0, tmem, warp >> 2, blockIdx.x);
+        cp_async_wait_all();   // after an abort, queries may be on their way still
     } else {
         if (warp == 8) rows_producer<D, kFmt>(p, &map, B, tiles, raw, lane);
         else if (warp < 11) {

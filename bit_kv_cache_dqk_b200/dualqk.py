@@ -28,7 +28,7 @@ EXPORTED = ["dqk_block_bytes", "dqk_append", "dqk_decode_workspace_size", "dqk_d
             "dqk_decode_noalloc", "dqk_bf16_block_bytes", "dqk_bf16_append",
             "dqk_bf16_decode_workspace_size", "dqk_bf16_decode", "dqk_rope_append", "dqk_bf16_rope_append",
             "dqk_prefix_decode_workspace_size", "dqk_prefix_decode", "dqk_bf16_prefix_decode_workspace_size",
-            "dqk_bf16_prefix_decode", "dqk_bf16_cross_attention_workspace_size", "dqk_bf16_cross_attention",
+            "dqk_bf16_prefix_decode", "dqk_test_prefix_stall", "dqk_bf16_cross_attention_workspace_size", "dqk_bf16_cross_attention",
             "dqk_last_device_error", "dqk_status_string"]
 
 DQK_NOALLOC_WORKSPACE_BYTES = 8 << 20
@@ -87,6 +87,9 @@ _lib.dqk_prefix_decode.argtypes = [_D, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P
 _lib.dqk_bf16_prefix_decode.restype = C.c_int
 _lib.dqk_bf16_prefix_decode.argtypes = [_D, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, C.c_int, _P, _P, C.c_int, _P,
                                         C.c_int, _P, C.c_size_t, _P]
+_lib.dqk_test_prefix_stall.restype = C.c_int
+_lib.dqk_test_prefix_stall.argtypes = [_D, C.c_int, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, C.c_int, _P, _P, C.c_int,
+                                       C.c_int, _P, C.c_int, _P, _P, C.c_size_t, _P]
 _lib.dqk_bf16_cross_attention_workspace_size.restype = C.c_size_t
 _lib.dqk_bf16_cross_attention_workspace_size.argtypes = [_D, C.c_int, C.c_int, C.c_int]
 _lib.dqk_bf16_cross_attention.restype = C.c_int
@@ -280,6 +283,19 @@ def dqk_bf16_prefix_decode(layer, q, q_dtype, batch, n_prefixes, prefix_start, p
                                      _addr(page_table), max_pages, _addr(out), out_dtype, _addr(workspace),
                                      workspace_bytes, _stream(stream))
     return _check(st, "dqk_bf16_prefix_decode", raise_on_error)
+
+
+def dqk_test_prefix_stall(layer, bf16, q, q_dtype, batch, n_prefixes, prefix_start, prefix_lens, prefix_table,
+                          max_prefix_pages, seq_lens, page_table, max_pages, sparsity_pct, out, out_dtype, sel_out,
+                          workspace, workspace_bytes, stream=None, raise_on_error=True) -> int:
+    """Test only: a shared-prefix decode with a stage that is never filled and
+    1 ms waits (see include/dualqk.h); the device error word then reads
+    DQK_ERR_TIMEOUT."""
+    st = _lib.dqk_test_prefix_stall(C.byref(layer), bf16, _addr(q), q_dtype, batch, n_prefixes, _addr(prefix_start),
+                                    _addr(prefix_lens), _addr(prefix_table), max_prefix_pages, _addr(seq_lens),
+                                    _addr(page_table), max_pages, sparsity_pct, _addr(out), out_dtype, _addr(sel_out),
+                                    _addr(workspace), workspace_bytes, _stream(stream))
+    return _check(st, "dqk_test_prefix_stall", raise_on_error)
 
 
 def dqk_bf16_cross_attention_workspace_size(layer, batch, total_q, max_pages) -> int:

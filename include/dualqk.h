@@ -403,6 +403,18 @@ dqk_status dqk_bf16_prefix_decode(const dqk_layer_desc *layer, const void *q, dq
                                   const int *page_table, int max_pages, void *out, dqk_dtype out_dtype, void *workspace,
                                   size_t workspace_bytes, dqk_stream_t stream);
 
+/* dqk_test_prefix_stall -- TEST ONLY: dqk_prefix_decode, or (bf16 != 0, without
+ * sparsity_pct and sel_out) dqk_bf16_prefix_decode, with a fault injected on
+ * the host's request, as in dqk_test_decode_stall: the producer warp of CTA 0
+ * never fills the stage of its second unit of 128 tokens and every wait gives up
+ * after 1 ms.  All roles of that CTA end, nothing stays in flight, and
+ * dqk_last_device_error() then returns DQK_ERR_TIMEOUT.  `out` is undefined. */
+dqk_status dqk_test_prefix_stall(const dqk_layer_desc *layer, int bf16, const void *q, dqk_dtype q_dtype, int batch,
+                                 int n_prefixes, const int *prefix_start, const int *prefix_lens,
+                                 const int *prefix_table, int max_prefix_pages, const int *seq_lens,
+                                 const int *page_table, int max_pages, int sparsity_pct, void *out, dqk_dtype out_dtype,
+                                 int16_t *sel_out, void *workspace, size_t workspace_bytes, dqk_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * dqk_bf16_cross_attention -- any number of query tokens per sequence against
  * that sequence's encoder states in the BF16 cache (filled by dqk_bf16_append),

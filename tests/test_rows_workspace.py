@@ -1,5 +1,5 @@
 """Workspace of the shared-prefix decode and the cross attention: sized by the
-row heads that exist (host side, no GPU needed)."""
+row heads that exist; refusals of the test-only stall (host side, no GPU needed)."""
 import itertools
 
 import pytest
@@ -60,3 +60,12 @@ def test_grows_with_every_size(Q, which):
         for axis in range(4):
             up = tuple(k + (axis == a) for a, k in enumerate(i))
             assert up not in got or got[up] >= x > 0, (i, up)
+
+
+def test_stall_is_refused_as_the_plain_calls(Q):
+    d = layer(Q)
+    for bf16 in (0, 1):
+        ok = [d, bf16, 256, Q.DQK_BF16, 4, 1, 256, 256, 256, 8, 256, 256, 2, 40, 256, Q.DQK_F32, None, 256, 64]
+        assert Q.dqk_test_prefix_stall(*ok, stream=0, raise_on_error=False) == Q.DQK_ERR_WORKSPACE_TOO_SMALL
+        bad = ok[:4] + [0] + ok[5:]
+        assert Q.dqk_test_prefix_stall(*bad, stream=0, raise_on_error=False) == Q.DQK_ERR_INVALID_ARG
