@@ -55,13 +55,12 @@ __global__ void __launch_bounds__(kQueryThreads) k_query_rows(
     {
         // thread = channel c of kPer of the heads
         const int c = t % D, n0 = t / D * kPer;
+        static_assert(NH % kPer == 0, "a thread's row heads");
         if (n0 < NH) {
             double acc[kPer];
-            if constexpr (NH % kPer == 0) {
-                dot_rows_pad<D, kPer>(sT, c, qin + n0, NH, acc);
+            dot_rows_pad<D, kPer>(sT, c, qin + n0, NH, acc);
 #pragma unroll
-                for (int n = 0; n < kPer; ++n) qpv[(n0 + n) * D + c] = __double2float_rn(acc[n]);
-            }
+            for (int n = 0; n < kPer; ++n) qpv[(n0 + n) * D + c] = __double2float_rn(acc[n]);
         }
     }
     __syncthreads();

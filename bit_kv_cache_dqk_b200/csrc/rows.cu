@@ -132,7 +132,10 @@ dqk_status run_rope_tile(RopeParams &p, cudaStream_t s) {
 // One row per CTA, or tiles of 16 or 64 rows: whichever takes least by what they measured (us at head_dim 128,
 // 148 SMs): a row per CTA 10 and 13 more per 7 CTAs of an SM, a wave of tiles of 16 rows 13 and 4 before the first, of
 // 64 rows 17 and 13.  E.g. 16 sequences, 8 kv heads: 1 row each 12, 15, 19; 8 rows 23, 15, 23; 64 rows 118, 57, 30;
-// 1 sequence of 256 rows 35, 17, 29.
+// 1 sequence of 256 rows 35, 17, 29; of 8192 rows 908, 393, 193.  The same rule serves head_dim 64, where all three
+// are 2 to 3 times faster: over 38 sizes its choice was the fastest, but for 64 sequences of 8 rows (28 us in tiles of 16
+// where a row per CTA takes 26); 1 sequence of 8192 rows 439, 205, 113, 16 of 64 rows 42, 31, 19, 64 of 1 row 13, 27, 41.
+// The lengths are on the device, so the rule goes by max_new.
 template <int D, int NS>
 dqk_status run_rope_int2(RopeParams &p, cudaStream_t s) {
     const int sms = device_sms(current_device());
@@ -291,7 +294,7 @@ dqk_status run_rows_kernels(const RowsCall &a, RowsParams &p, const RowsPlanHost
     p.vtiles = tiles - p.ktiles;
     // page flags: at most kRowsFlags units between their copies and the softmax
     constexpr size_t kCh0 = T::kInt2 ? kRowsCh0 * rows_ch0_bytes(VCH0) : 0;
-    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(3, (kRoom - 4 * T::kTile - kCh0) / (kRowsPages * P.bb)) : 0;
+    p.raw_stages = T::kInt2 ? (int)std::min<size_t>(kRowsMaxRaw, (kRoom - 4 * T::kTile - kCh0) / (kRowsPages * P.bb)) : 0;
     const size_t smem = 1024 + 2 * T::kParts * T::kTile + (size_t)tiles * T::kTile + (size_t)p.raw_stages * kRowsPages * P.bb + kCh0;
     dqk_status st = prepare_kernel<k_rows<D, kFmt, kW, NS, VCH0>>(dev, smem, T::kThreads);
     if (st != DQK_OK) return st;
@@ -326,8 +329,8 @@ dqk_status launch_query_rows(const RowsCall &a, const RowsParams &p, int dev, ui
 template <int D, int G>
 dqk_status run_query_rows(const RowsCall &a, const RowsParams &p, int dev, uint16_t *rows, float2 *head) {
     // four rows per staged transform once one row each makes more than three CTAs per SM: the whole decode with 1 and
-    // 4 (us; 8 kv heads, 1024 shared tokens) 38 and 42 at 32 rows, 49 and 51 at 48, 63 and 59 at 64, 97 and 93 at 128
-    return (long long)p.total_rows * p.hkv > 3 * 148 ? launch_query_rows<D, G, 4>(a, p, dev, rows, head)
+    // 4 (us; 148 SMs, 8 kv heads, 1024 shared tokens) 38 and 42 at 32 rows, 49 and 51 at 48, 63 and 59 at 64, 97 and 93 at 128
+    return (long long)p.total_rows * p.hkv > 3LL * device_sms(dev) ? launch_query_rows<D, G, 4>(a, p, dev, rows, head)
                                                      : launch_query_rows<D, G, 1>(a, p, dev, rows, head);
 }
 

@@ -573,7 +573,7 @@ __host__ __device__ __forceinline__ int rows_channel_pos(int c) {
 // along the row.  Behind the packed blocks: channel 0 of a unit's keys and (protected) of its values in fp32,
 // [unit modulo kRowsCh0][keys, values][half][page][8 tokens], 0 where no token is.
 // ---------------------------------------------------------------------------
-constexpr int kRowsMaxTiles = 8, kRowsMaxRaw = 8;
+constexpr int kRowsMaxTiles = 8, kRowsMaxRaw = 3;
 // Units whose channel 0 is held.  A unit's is written once the key tile of two units before (INT2 has two) is free:
 // both warpgroups have then formed scores of the two units before it, so they are through with all units before those.
 constexpr int kRowsCh0 = 4;
@@ -591,7 +591,6 @@ struct RowsBars {
     int abort;
     RowsCursor cursor;
 };
-__host__ __device__ constexpr size_t rows_tile_bytes(int D) { return (size_t)kRowsKv * D * 2; }
 
 template <int D, int kFmt>
 struct RowsShape {
