@@ -326,11 +326,12 @@ __device__ __forceinline__ uint32_t rows_record(const RowsParams &p, int cta, ui
 __device__ __forceinline__ uint32_t rows_heads_before(const RowsParams &p, int row0, int first, int rows, int j) {
     return (uint32_t)(row0 * p.G + first) * p.hkv + (uint32_t)(j * rows);
 }
-// A record's place in its segment: row head x of a tile that both warpgroups take, or warpgroup g's of row head x.
-__device__ __forceinline__ uint32_t rows_place(bool both, int x, int g) { return (uint32_t)(both ? x : 2 * x + g); }
+// A record's place in its segment of n row heads: row head x of a tile that both warpgroups take, or warpgroup g's of row
+// head x (one warpgroup's behind the other's: 53.4 -> 51.7 us on a chat batch against the two of a row head side by side).
+__device__ __forceinline__ uint32_t rows_place(bool both, int x, int g, int n) { return (uint32_t)(both ? x : g * n + x); }
 // Own lists: CTA + item, two records of each of the G row heads.
 __device__ __forceinline__ uint32_t rows_own_record(const RowsParams &p, int cta, int row, int j, int x, int g) {
-    return (uint32_t)(cta + row * p.hkv + j) * 2 * p.G + rows_place(false, x, g);
+    return (uint32_t)(cta + row * p.hkv + j) * 2 * p.G + rows_place(false, x, g, p.G);
 }
 __device__ __forceinline__ float *rows_at(float *rec, uint32_t record, int D) { return rec + (size_t)record * rec_stride(D); }
 
@@ -767,18 +768,18 @@ __device__ __forceinline__ void rows_unpack(const RowsParams &p, RowsBars &B, un
             if (!ok) break;
             const uint32_t have = B.flags[unit & (kRowsFlags - 1)];
             const uint32_t blk = smem_addr(raw) + (uint32_t)(rs * kRowsPages * p.bb);
+            {   // channel 0 of the warp's two pages
+                const int pg = warp + kRowsUnpackWarps * (lane / kPage), t = lane % kPage;
+                const uint32_t at = ch0 + (uint32_t)(unit & (kRowsCh0 - 1)) * rows_ch0_bytes(VCH0) +
+                                    (uint32_t)((t >> 3) * (kRowsKv * 2) + pg * 32 + (t & 7) * 4);
+                const bool token = ((have >> pg) & 1u) && kPage * pg + t < nv;
+                st_s32(at, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.k0 + 2 * k0_idx(t))) << 16 : 0u);
+                if constexpr (VCH0)
+                    st_s32(at + kRowsKv * 4, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.v0 + 2 * t)) << 16 : 0u);
+            }
 #pragma unroll 1
-            for (int pg = warp; pg < kRowsPages; pg += kRowsUnpackWarps) {
-                const bool in = (have >> pg) & 1u;
-                if (lane < kPage) {
-                    const uint32_t at = ch0 + (uint32_t)(unit & (kRowsCh0 - 1)) * rows_ch0_bytes(VCH0) +
-                                        (uint32_t)((lane >> 3) * (kRowsKv * 2) + pg * 32 + (lane & 7) * 4);
-                    const bool token = in && kPage * pg + lane < nv;
-                    st_s32(at, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.k0 + 2 * k0_idx(lane))) << 16 : 0u);
-                    if constexpr (VCH0)
-                        st_s32(at + kRowsKv * 4, token ? ld_s16(blk + (uint32_t)(pg * p.bb + kL.v0 + 2 * lane)) << 16 : 0u);
-                }
-                if (!in) continue;   // its scores are masked
+            for (int pg = warp; pg < pages; pg += kRowsUnpackWarps) {
+                if (!((have >> pg) & 1u)) continue;   // its scores are masked
                 PageInt2<D, NS> b;
                 b.load_keys(blk + (uint32_t)(pg * p.bb), lane);
                 const uint32_t row = tile0 + (uint32_t)sk * kTile + ka + (uint32_t)pg * 1024;
@@ -1126,7 +1127,7 @@ __device__ __forceinline__ float rows_largest(uint32_t tS, float qs, const RowsK
 // has moved and what was summed -- l, z, and the accumulator, once `settled` has waited for it -- has been rescaled.
 // Channel 0 of the INT2 cache does not go through fp16, which would round it below 2^-14 and cut it off at 65504: the
 // keys' is added to the scores, the products with the values' (z, protected) are summed, both in fp32.  That costs 4 %
-// (64 sequences behind 128K tokens 286 and 297 us, a chat batch 50.1 and 52.3).
+// (64 sequences behind 128K tokens 286 and 300 us, a chat batch 49.9 and 51.7).
 template <int D, bool F16, int kW, bool VCH0, typename Settled>
 __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, const RowsKey0 &ch, float lift, float &m,
                                           float &l, float &z, Settled settled) {
@@ -1329,7 +1330,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             float f = 1.0f, f1 = 0.0f;
             const float *other = nullptr;
             if (joint) {
-                other = record(rows_place(false, r, 1));
+                other = record(rows_place(false, r, 1, s.rows()));
                 ok = __all_sync(0xffffffffu, rows_wait(&B.join, jn & 1, B, p.wait_ns));
                 ++jn;
                 if (!ok) return;
@@ -1383,7 +1384,7 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
             if (joint && lane == 0) mbar_arrive(&B.read);
         } else {
             float *rec = s.own(p) ? rows_at(p.own_rec, rows_own_record(p, cta, s.row0, s.j, r, w), D)
-                                  : record(rows_place(s.both(), s.both() ? kRowsHalf * w + r : r, w));
+                                  : record(rows_place(s.both(), s.both() ? kRowsHalf * w + r : r, w, s.rows()));
             if (t.valid) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);   // no unit of this segment: (-inf, 0) alone
             if (t.any && t.mine) {
 #pragma unroll 2
@@ -1530,10 +1531,9 @@ struct RowsMerge {
 #pragma unroll
         for (int e = 0; e < V; ++e) O[e] = none ? O[e] : fmaf(f, o[e], O[e]);
     }
-    // The records of row head r of an item whose first unit begins at `start`: CTAs cf .. cl, both
-    // warpgroups' where the units went to one and the other.  before: rows_heads_before of the item, or (own) its query row.
-    __device__ __forceinline__ void take(const RowsParams &p, bool own, long long start, int per, bool both, long long q,
-                                         uint32_t before, int j, int r, int lane) {
+    // The records of a row head of an item whose first unit begins at `start`: CTAs cf .. cl, both warpgroups' where
+    // the units went to one and the other.  A CTA's lie at rec + CTA step, the second warpgroup's `second` behind.
+    __device__ __forceinline__ void take(const float *rec, int step, int second, long long start, int per, bool both, long long q, int lane) {
         if (per <= 0) return;
         const int w = both ? kRowsBothCost : kRowsOneCost, shares = both ? 1 : 2;
         const int cf = (int)rows_div(start, q), cl = (int)rows_div(start + (long long)(per - 1) * w, q), n = (cl - cf + 1) * shares;
@@ -1543,18 +1543,14 @@ struct RowsMerge {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k;
-                const int c = cf + i / shares;
+                const int c = cf + (both ? i : i >> 1);
                 m[k] = -INFINITY;
                 l[k] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[k][e] = 0.0f;
                 // (no unit need begin in a short range)
                 const bool has = rows_begun(c * q - start, w, per) < rows_begun((c + 1) * q - start, w, per);
-                if (i < n && has) {
-                    load(own ? rows_at(p.own_rec, rows_own_record(p, c, (int)before, j, r, i & 1), D)
-                             : rows_at(p.rec, rows_record(p, c, before, c == cf) + rows_place(both, r, i & 1), D),
-                         lane, m[k], l[k], o[k]);
-                }
+                if (i < n && has) load(rec + (size_t)(c * step + (both ? 0 : (i & 1) * second)) * rec_stride(D), lane, m[k], l[k], o[k]);
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) to = fmaxf(to, m[k]);
@@ -1606,11 +1602,14 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
         const long long first = p.plan->first[g];
         const int row0 = rows_first(p, g), heads = (rows_first(p, g + 1) - row0) * p.G;
         const int rr = (row - row0) * p.G + hh, mt = rr / kRowsTile, w = mt < r.tiles - 1 ? kRowsBothCost : r.last;
-        acc.take(p, false, first + (long long)mt * p.hkv * rows_cost(p, r.per, kRowsBothCost) + j * rows_cost(p, r.per, w) + p.head,
-                 r.per, w == kRowsBothCost, q, rows_heads_before(p, row0, mt * kRowsTile, min(kRowsTile, heads - mt * kRowsTile), j), j,
-                 rr - mt * kRowsTile, lane);
+        const bool both = w == kRowsBothCost;
+        const uint32_t before = rows_heads_before(p, row0, mt * kRowsTile, min(kRowsTile, heads - mt * kRowsTile), j);
+        acc.take(rows_at(p.rec, rows_record(p, 0, before, false) + rows_place(both, rr - mt * kRowsTile, 0, 0), D), (int)p.rec_step, min(kRowsTile, heads - mt * kRowsTile),
+                 first + (long long)mt * p.hkv * rows_cost(p, r.per, kRowsBothCost) + j * rows_cost(p, r.per, w) + p.head, r.per, both,
+                 q, lane);
     }
-    acc.take(p, true, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head, per, false, q, row, j, hh, lane);
+    acc.take(rows_at(p.own_rec, rows_own_record(p, 0, row, j, hh, 0), D), 2 * p.G, p.G, own_first + j * rows_cost(p, per, kRowsOneCost) + p.head,
+             per, false, q, lane);
     acc.store(p, (size_t)row * p.hq + h, lane);
 }
 
@@ -1653,7 +1652,7 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
     const uint32_t step_cta = p.rec_pairs ? 2 * p.rec_step : p.rec_step;
     uint32_t place[kRowsMergeHeads];
 #pragma unroll
-    for (int k = 0; k < kRowsMergeHeads; ++k) place[k] = rows_place(both, min(x0 + k * step, heads - 1), 0);
+    for (int k = 0; k < kRowsMergeHeads; ++k) place[k] = rows_place(both, min(x0 + k * step, heads - 1), 0, 0);
     const int cl = (int)rows_div(c.start + (long long)(r.per - 1) * w, q);
     const int shares = both ? 1 : 2, n = (cl - b + 1) * shares;
     for (int i0 = 0; i0 < n; i0 += 2) {   // two records of every row head at a time
@@ -1665,7 +1664,7 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const
             has[e] = i0 + e < n && rows_begun(a * q - c.start, w, r.per) < rows_begun((a + 1) * q - c.start, w, r.per);
 #pragma unroll
             for (int k = 0; k < kRowsMergeHeads; ++k)   // (a record that was not written is inside the workspace too)
-                RowsMerge<D>::load(rows_at(p.rec, (a == b ? here : next + (uint32_t)(a - b - 1) * step_cta) + place[k] + g, D), lane, m[e][k],
+                RowsMerge<D>::load(rows_at(p.rec, (a == b ? here : next + (uint32_t)(a - b - 1) * step_cta) + place[k] + g * heads, D), lane, m[e][k],
                                    l[e][k], o[e][k]);
         }
 #pragma unroll
