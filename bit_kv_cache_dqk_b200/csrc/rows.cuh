@@ -33,14 +33,16 @@
 // half's scores into weights, the tensor core takes the other half's weights and
 // forms the next job's scores.
 //
-// What bounds it.  Many row heads: the softmax warpgroups.  A unit of 256 row heads takes 4300 clocks
-// (BF16, head_dim 128), of which the products are 2050 and the 32768 powers of two 2050 of their units;
-// a half of 64 tokens is 1100 clocks of arithmetic and 900 of waiting, reading and writing TMEM.  INT2 takes 5240, since four
-// warps that unpack (they have the registers for no more) keep pace with neither.  Few row heads: the chain
-// key tile - scores - weights - values of a unit, 2630 clocks with two units in flight, and DRAM.  4 x 1024 queries over 4096
-// states (169 GFLOP): 221 us, 0.76 PFLOP/s; 64 sequences behind 128K tokens, INT2 (110 GFLOP): 282 us; 32
-// sequences behind two documents of 32K tokens, BF16 (354 MB): 88 us, 4.0 TB/s; one query token each for 16
-// sequences of 1500 states (74 MB): 30 us, of which about 6 us are the start.
+// What bounds it.  Many row heads: the hand-over between the softmax warpgroups and the tensor core.  A unit of 256
+// row heads takes 4300 clocks (BF16, head_dim 128), of which the products are 2050 and the 32768 powers of two 2050 of
+// their units (both are busy 41 % of the time on the cross attention below); a half of 64 tokens is 1100 clocks of
+// arithmetic and 900 of waiting, reading and writing TMEM.  INT2 takes about 5500: the four warps that unpack keep pace
+// with neither, the softmax threads spill at their 128 registers, and CTAs of equal work differ by up to 40 %.  Few row
+// heads: the chain key tile - scores - weights - values of a unit, 2630 clocks with two units in flight, and DRAM.
+// Cross attention of 4 sequences of 540 to 1024 queries over 2121 to 4096 states (169 GFLOP): 218 us, 0.77 PFLOP/s; 64
+// sequences behind 128K tokens, INT2 (110 GFLOP): 301 us; 32 sequences behind two documents of up to 32K tokens, BF16
+// (354 MB): 84 us, 4.2 TB/s; one query token each for 16 sequences of 750 to 1500 states (74 MB): 30 us, of which about 6
+// are the start.  Every instance with BF16 weights of one part or INT2 spills a few registers (42 to 92 bytes of stores).
 #pragma once
 
 #include <cuda.h>
@@ -109,9 +111,9 @@ __device__ __forceinline__ int rows_first(const RowsParams &p, int g) {
 
 // The work is split by cost: of a unit that both warpgroups take, of one that goes to one of them, and of
 // an item besides (p.head: its queries, its outputs, the pipeline's end and start).  A CTA's clocks, head_dim
-// 128: BF16 4300, 2630 and 4600; INT2 5240, 3500 and 2800; but units of one list beside others' are
-// slower, and the ratios are those that measured best (us; cross attention of 4 x 1024 queries over 4096 states, two
-// documents of 32K tokens, INT2 document of 128K): 2 : 1 : 0 312, 96, 359; 3 : 2 : 3 or 2 247, 83, 282;
+// 128: BF16 4300, 2630 and 4600; INT2 5500, 3500 and 2800; but units of one list beside others' are
+// slower, and the ratios are those that measured best when they were chosen (us; the three largest cases above: cross
+// attention, two documents, INT2 document): 2 : 1 : 0 312, 96, 359; 3 : 2 : 3 or 2 247, 83, 282;
 // 5 : 4 : 6 or 4 218, 82, 285; 5 : 4 : 9 or 6 218, 82, 286 and less for short lists; 9 : 8 : 12 or 8 217, 83, 288.
 constexpr int kRowsBothCost = 5, kRowsOneCost = 4, kRowsHeadBf16 = 9, kRowsHeadInt2 = 6;
 
@@ -1616,8 +1618,8 @@ __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge(const __gri
 // Without own lists, CTA (b, y): row heads 8 y .., a warp each, and those 8 gridDim.y further on, of the item that
 // begins in CTA b of the row kernel and goes on in the next one (every other item's outputs are written already); the
 // CTAs behind those zero the rows of groups without any token (and, zero_rest, of no group).
-// What bounds it is the arithmetic of the items and records, which the warp's row heads share (cross attention of 4 x
-// 1024 queries over 4096 states, all kernels, with 1, 2 and 4 of them: 213, 204, 208 us).
+// What bounds it is the arithmetic of the items and records, which the warp's row heads share (cross attention of up to
+// 1024 queries over up to 4096 states, all kernels, with 1, 2 and 4 of them: 220, 218, 218 us).
 constexpr int kRowsMergeHeads = 2;
 template <int D>
 __global__ void __launch_bounds__(32 * kRowsMergeWarps) k_rows_merge_items(const __grid_constant__ RowsParams p) {

@@ -355,9 +355,20 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
 
 /* ---------------------------------------------------------------------------
  * Decode of a batch that shares long prefixes: every sequence attends its
- * prefix's tokens and then its own, and a prefix is read once for all its
- * sequences.  (dqk_decode over a page table that repeats the prefix's pages
- * gives the same attention and reads them once per sequence.)
+ * prefix's tokens and then its own, and a prefix is read once for each 256 row
+ * heads (sequences times Hq / Hkv) that share it.
+ *
+ * dqk_decode and dqk_bf16_decode over page tables that repeat a prefix's pages
+ * (prefixes of whole pages) give the same attention and read them once per
+ * sequence.  Which is faster depends on how many sequences share how much.  This
+ * call and that one, us on a B200, 32 / 8 heads, d = 128:
+ *   INT2: 298 and 1159 for 64 sequences behind 128K tokens; 84 and 93 for 16 behind
+ *   32K; 111 and 120 for 64 behind 8K; but 51 and 40 for 16 behind 8K with 1000
+ *   tokens of their own, 43 and 25 for 4 of them, 102 and 39 for 8 prefixes of two
+ *   sequences.  Worth it from 16 sequences behind 32K tokens or 64 behind 8K.
+ *   BF16: 80 and 370 for 32 sequences behind two prefixes of 32K; 27 and 58 for 16
+ *   behind 8K; 21 and 23 for 8 behind 2K; 19 and 18 for two; 57 and 52 for prefixes
+ *   of one sequence each.  Worth it from about 4 sequences per prefix.
  *
  *  q                (device) [batch][Hq][d], 16-byte aligned, RoPE applied.
  *  prefix_start     (device) int [n_prefixes + 1], ascending: sequences
@@ -430,6 +441,9 @@ dqk_status dqk_test_prefix_stall(const dqk_layer_desc *layer, int bf16, const vo
  *  page_table    (device) int [batch][max_pages].
  *  out           (device) [total_q][Hq][d] in out_dtype, 16-byte aligned.
  *  Precision and errors as in dqk_bf16_prefix_decode.
+ *  With one query row per sequence and fp32 outputs this is dqk_bf16_decode, which
+ *  is as fast or faster there: 23 us against 28 for 16 sequences of up to 1500
+ *  states, 63 and 79 for 64, 19 and 19 for 4.
  * ------------------------------------------------------------------------- */
 size_t dqk_bf16_cross_attention_workspace_size(const dqk_layer_desc *layer, int batch, int total_q, int max_pages);
 dqk_status dqk_bf16_cross_attention(const dqk_layer_desc *layer, const void *q, dqk_dtype q_dtype, int batch,
