@@ -37,12 +37,13 @@
 // row heads takes 4300 clocks (BF16, head_dim 128), of which the products are 2050 and the 32768 powers of two 2050 of
 // their units (both are busy 41 % of the time on the cross attention below); a half of 64 tokens is 1100 clocks of
 // arithmetic and 900 of waiting, reading and writing TMEM.  INT2 takes about 5500: the four warps that unpack keep pace
-// with neither, the softmax threads spill at their 128 registers, and CTAs of equal work differ by up to 40 %.  Few row
+// with neither, and CTAs of equal work differ by up to 40 %.  Few row
 // heads: the chain key tile - scores - weights - values of a unit, 2630 clocks with two units in flight, and DRAM.
 // Cross attention of 4 sequences of 540 to 1024 queries over 2121 to 4096 states (169 GFLOP): 218 us, 0.77 PFLOP/s; 64
-// sequences behind 128K tokens, INT2 (110 GFLOP): 301 us; 32 sequences behind two documents of up to 32K tokens, BF16
-// (354 MB): 84 us, 4.2 TB/s; one query token each for 16 sequences of 750 to 1500 states (74 MB): 30 us, of which about 6
-// are the start.  Every instance with BF16 weights of one part or INT2 spills a few registers (42 to 92 bytes of stores).
+// sequences behind 128K tokens, INT2 (110 GFLOP): 300 us; 32 sequences behind two documents of up to 32K tokens, BF16
+// (354 MB): 86 us, 4.1 TB/s; one query token each for 16 sequences of 750 to 1500 states (74 MB): 30 us, of which about 6
+// are the start.  The BF16 instances with weights of one part and the INT2 ones with a protected value channel 0 spill a
+// few registers (42 to 46 and 74 to 82 bytes of stores).
 #pragma once
 
 #include <cuda.h>
@@ -417,6 +418,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+                 : "memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *r) {
 #define DQK_IN(i) "r"(r[i])
@@ -1128,8 +1134,8 @@ __device__ __forceinline__ float rows_largest(uint32_t tS, float qs, const RowsK
 // whose scores pass the reference by more than the slack (rare) is taken again after the reference
 // has moved and what was summed -- l, z, and the accumulator, once `settled` has waited for it -- has been rescaled.
 // Channel 0 of the INT2 cache does not go through fp16, which would round it below 2^-14 and cut it off at 65504: the
-// keys' is added to the scores, the products with the values' (z, protected) are summed, both in fp32.  That costs 4 %
-// (64 sequences behind 128K tokens 286 and 300 us, a chat batch 49.9 and 51.7).
+// keys' is added to the scores, the products with the values' (z, protected) are summed, both in fp32.  That costs 1 to 5 %
+// (64 sequences behind 128K tokens 286 and 300 us, a chat batch 49.9 and 50.3).
 template <int D, bool F16, int kW, bool VCH0, typename Settled>
 __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, float qs, const RowsKey0 &ch, float lift, float &m,
                                           float &l, float &z, Settled settled) {
@@ -1154,6 +1160,7 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, 
     }
     const float mx = F16 ? a.largest() + base : a.largest() * qs;
     const bool move = valid && mx > m + kRowsSlack;   // (lanes without a row hold anything)
+    bool stored = false;
     if (__any_sync(0xffffffffu, move)) {
         // the references are whole numbers: moving one scales by a power of two
         const float to = move ? ceilf(mx) : m, f = !move || m == -INFINITY ? 1.0f : fast_exp2(m - to);
@@ -1166,18 +1173,32 @@ __device__ __forceinline__ bool rows_half(uint32_t tS, uint32_t tO, bool valid, 
         base = (m == -INFINITY ? 0.0f : m) - lift;
         b2 = make_float2(-base, -base);
         a.clear();
+        if constexpr (F16) {   // (a loop, for little code and no spills: weights go to columns whose scores have been taken)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t y[16], w[8];
+                tm_ld16(tS + 16 * c, y);
+                tm_ready16(y);
+                rows_weights<F16, kW, VCH0>(y, q2, b2, ch.at(c), w, a);
+                tm_st8(tS + 8 * c, w);
+            }
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t y[16];
-            tm_ld16(tS + 16 * c, y);
-            tm_ready16(y);
-            rows_weights<F16, kW, VCH0>(y, q2, b2, ch.at(c), pk + 8 * c, a);
+            for (int c = 0; c < 4; ++c) {
+                uint32_t y[16];
+                tm_ld16(tS + 16 * c, y);
+                tm_ready16(y);
+                rows_weights<F16, kW, VCH0>(y, q2, b2, ch.at(c), pk + 8 * c, a);
+            }
         }
+        stored = F16;
     }
     l += (a.s0.x + a.s0.y) + (a.s1.x + a.s1.y);
     if constexpr (VCH0) z += (a.z0.x + a.z0.y) + (a.z1.x + a.z1.y);
+    if (!stored) {
 #pragma unroll
-    for (int i = 0; i < 2 * kW; ++i) tm_st16(tS + 16 * i, pk + 16 * i);
+        for (int i = 0; i < 2 * kW; ++i) tm_st16(tS + 16 * i, pk + 16 * i);
+    }
     tm_wait_st();
     return true;
 }

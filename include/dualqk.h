@@ -362,9 +362,9 @@ dqk_status dqk_bf16_rope_append(const dqk_layer_desc *layer, const dqk_rope_desc
  * (prefixes of whole pages) give the same attention and read them once per
  * sequence.  Which is faster depends on how many sequences share how much.  This
  * call and that one, us on a B200, 32 / 8 heads, d = 128:
- *   INT2: 298 and 1159 for 64 sequences behind 128K tokens; 84 and 93 for 16 behind
- *   32K; 111 and 120 for 64 behind 8K; but 51 and 40 for 16 behind 8K with 1000
- *   tokens of their own, 43 and 25 for 4 of them, 102 and 39 for 8 prefixes of two
+ *   INT2: 299 and 1156 for 64 sequences behind 128K tokens; 83 and 93 for 16 behind
+ *   32K; 111 and 119 for 64 behind 8K; but 51 and 41 for 16 behind 8K with 1000
+ *   tokens of their own, 42 and 26 for 4 of them, 100 and 39 for 8 prefixes of two
  *   sequences.  Worth it from 16 sequences behind 32K tokens or 64 behind 8K.
  *   BF16: 80 and 370 for 32 sequences behind two prefixes of 32K; 27 and 58 for 16
  *   behind 8K; 21 and 23 for 8 behind 2K; 19 and 18 for two; 57 and 52 for prefixes
