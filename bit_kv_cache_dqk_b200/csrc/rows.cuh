@@ -1444,9 +1444,9 @@ __device__ __forceinline__ void rows_softmax(const RowsParams &p, RowsBars &B, u
 // kFmt: BF16 cache with BF16 (0) or fp32 queries (1), INT2 cache (2); kW: parts of a softmax weight.
 // A BF16 output is rounded by half a step, 2^-8, itself, and so may the weights be, each for itself (against
 // 64 bits 0.0023 where the output's rounding alone leaves 0.0017); an fp32 output gets weights of two parts, 2^-16, as in
-// dqk_bf16_decode (3e-6 where one part leaves 0.0017).  The second product costs 16 % where the softmax warpgroups
-// bound (up to 1024 queries over up to 4096 states, fp32 out: 225 and 262 us), 6 % on long documents (81 and 86) and
-// up to 2 us of the smallest calls.
+// dqk_bf16_decode (3e-6 where one part leaves 0.0017).  The second product costs 12 to 16 % where many row heads bound
+// (up to 1024 queries over up to 4096 states, fp32 out: 225 and 253 to 262 us), 4 to 6 % on long documents (81 and 84
+// to 86) and up to 3 us of the smallest calls.
 template <int D, int kFmt, int kW, int NS, bool VCH0>
 __global__ void __launch_bounds__(RowsShape<D, kFmt>::kThreads, 1)
     k_rows(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap map) {

@@ -20,37 +20,27 @@ pytestmark = pytest.mark.gpu
 
 class Scaled(R.Lists):
     def __init__(self, factor, *a, **kw):
-        self.factor = np.float32(factor)
+        self.factor, self.transforms_scaled = np.float32(factor), False
         super().__init__("int2", *a, **kw)
 
     def _append(self, table, lens, ks, vs, dtype):
-        if self.factor != 1:
+        if not self.transforms_scaled:      # the second set of lists is appended with the same ones
             self.t_k[:, 0, :] *= self.factor
             self.t_q[:, 0, :] /= self.factor
             self.tk_dev.copy_(torch.from_numpy(self.t_k))
             self.tq_dev.copy_(torch.from_numpy(self.t_q))
+            self.transforms_scaled = True
         if self.v_ch0:
             for i, v in enumerate(vs):
                 vs[i] = v.clone()
-                vs[i][..., 0] *= float(self.factor0)
-        self.factor = np.float32(1)     # the second set of lists is appended with the same transforms
+                vs[i][..., 0] *= float(self.factor)
         super()._append(table, lens, ks, vs, dtype)
-
-    @property
-    def factor0(self):
-        return self._f0
-
-    _f0 = 1.0
-
-
-def scaled(factor, *a, **kw):
-    return type("Scaled", (Scaled,), {"_f0": factor})(factor, *a, **kw)
 
 
 @pytest.mark.parametrize("factor", [2.0 ** -20, 2.0 ** -60, 2.0 ** 20, 2.0 ** 60], ids=["2^-20", "2^-60", "2^20", "2^60"])
 @pytest.mark.parametrize("d,gs,v_ch0", [(128, 32, 0), (128, 128, 1), (64, 32, 1), (64, 64, 0)])
 def test_channel_0_of_any_magnitude(d, gs, v_ch0, factor):
-    L = scaled(factor, [[300, 18], [5, 0, 130, 16, 33]], 8, 2, d, gs=gs, v_ch0=v_ch0, seed=31)
+    L = Scaled(factor, [[300, 18], [5, 0, 130, 16, 33]], 8, 2, d, gs=gs, v_ch0=v_ch0, seed=31)
     q = queries(L, 5, scale=2.0)
     check_prefix(L, q, "bf16", [0, 3, 5])
     check_prefix(L, q, "f32", [0, 3, 5], own=False)
@@ -59,13 +49,13 @@ def test_channel_0_of_any_magnitude(d, gs, v_ch0, factor):
 @pytest.mark.parametrize("v_ch0", [0, 1])
 def test_many_row_heads(v_ch0):
     """Tiles of more than 128 row heads, items that several CTAs share."""
-    L = scaled(2.0 ** -20, [[3000], [n % 9 for n in range(40)]], 16, 2, 128, v_ch0=v_ch0, seed=32)
+    L = Scaled(2.0 ** -20, [[3000], [n % 9 for n in range(40)]], 16, 2, 128, v_ch0=v_ch0, seed=32)
     check_prefix(L, queries(L, 40, scale=2.0), "bf16", [0, 40])
 
 
 def test_stale_channel_0_behind_the_lists():
     """Infinities and NaN in the channel 0 slots behind a list's end, and an absent page, reach nothing."""
-    L = scaled(1.0, [[37], [3, 0]], 8, 2, 128, v_ch0=1, seed=33)
+    L = Scaled(1.0, [[37], [3, 0]], 8, 2, 128, v_ch0=1, seed=33)
     bb = L.bb
     blk = L.pool.view(L.num_pages, 2, bb)
     for table, lens in zip(L.tables, L.lens_list):
